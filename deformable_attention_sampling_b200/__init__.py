@@ -11,6 +11,12 @@ binding: it marshals pointers, sizes and streams and runs nothing itself.
     gx, goff, gmask = dcnb.dcn_grad(x, offset, mask, grad_out)
     gv, gloc, gattn = dcnb.msda_grad(value, shapes, starts, loc, attn, grad_out)
     out = dcnb.dynconv(x, weights, K)        # ContMix core: per-pixel K x K kernels
+
+and the operators of the attention block around them, each with its gradient:
+
+    q = dcnb.axial_rope(q, pos, freqs, axis_pairs)        # rotary positions, 1 to 4 axes
+    out, saved = dcnb.diff_attn(q, k, v, lam, save=True)  # difference of two softmax maps
+    z, h = dcnb.norm_residual(x, y, scale, gate)          # normed, gated residual join
 """
 from ._binding import (  # noqa: F401
     ALGO_CODES,
@@ -25,10 +31,17 @@ from ._binding import (  # noqa: F401
     DCN_ERR_MISALIGNED,
     DCN_ERR_UNSUPPORTED,
     DCN_OK,
+    DCN_NORM_POST,
+    DCN_NORM_PRE,
+    DCN_NORM_RMS,
     DTYPE_CODES,
     LIB_PATH,
     SIGNATURES,
     DcnError,
+    axial_rope,
+    axial_rope_backward,
+    axial_rope_forward,
+    axial_rope_grad,
     dcn,
     STATIC_SCRATCH_BYTES,
     dcn_backward,
@@ -54,6 +67,12 @@ from ._binding import (  # noqa: F401
     dcnv4_fused_forward_algo,
     dcn_status_string,
     dcn_version,
+    diff_attn,
+    diff_attn_backward,
+    diff_attn_backward_workspace_size,
+    diff_attn_forward,
+    diff_attn_forward_workspace_size,
+    diff_attn_grad,
     dtype_code,
     dynconv,
     dynconv_forward,
@@ -68,4 +87,9 @@ from ._binding import (  # noqa: F401
     msda_points,
     mask_value,
     msda_grad,
+    norm_residual,
+    norm_residual_backward,
+    norm_residual_backward_workspace_size,
+    norm_residual_forward,
+    norm_residual_grad,
 )

@@ -25,6 +25,9 @@ DTYPE_CODES = {"f32": 0, "f16": 1, "bf16": 2}
 DCN_FLAG_WAIT_TIMEOUT = 1
 DCN_FLAG_OUT_OF_BOUNDS = 2
 DCN_FLAG_BAD_LEVELS = 4
+DCN_NORM_RMS = 1
+DCN_NORM_POST = 2
+DCN_NORM_PRE = 4
 # the entry points the debug library holds (the forward calls and the status calls)
 DEBUG_SYMBOLS = ("dcn_forward", "dcn_forward_algo", "dcn_forward_plan", "dcnv4_fused_forward",
                  "dcnv4_fused_forward_algo", "msda_forward", "msda_forward_points",
@@ -61,6 +64,17 @@ SIGNATURES = {
     "dynconv_forward_algo": (_I, [_VP] * 3 + [_I] * 9 + [_VP]),
     "dcnv4_fused_forward": (_I, [_VP] * 4 + [_I] * 10 + [_VP]),
     "dcnv4_fused_forward_algo": (_I, [_VP] * 4 + [_I] * 11 + [_VP]),
+    "axial_rope_forward": (_I, [_VP] * 5 + [_I] * 6 + [_LL] * 2 + [_I] * 3 + [_VP]),
+    "axial_rope_backward": (_I, [_VP] * 7 + [_I] * 6 + [_LL] * 2 + [_I] * 3 + [_VP]),
+    "norm_residual_forward": (_I, [_VP] * 10 + [_I, _LL, _I, _I, ctypes.c_float, _I, _VP]),
+    "norm_residual_backward_workspace_size": (_LL, [_I, _LL, _I, _I, _I]),
+    "norm_residual_backward": (_I, [_VP] * 18 + [_LL, _I, _LL, _I, _I, ctypes.c_float, _I, _VP]),
+    "diff_attn_forward_workspace_size": (_LL, [_I] * 8),
+    "diff_attn_forward": (_I, [_VP] * 10 + [_LL] + [_I] * 7 + [_LL] * 6 +
+                          [ctypes.c_float, _I, _I, _VP]),
+    "diff_attn_backward_workspace_size": (_LL, [_I] * 4),
+    "diff_attn_backward": (_I, [_VP] * 15 + [_LL] + [_I] * 7 + [_LL] * 6 +
+                           [ctypes.c_float, _I, _I, _VP]),
     "dcn_output_size": (_I, [_I] * 5),
     "dcn_status_string": (ctypes.c_char_p, [_I]),
     "dcn_last_cuda_error": (_I, []),
@@ -141,6 +155,13 @@ def _stream(s):
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
+
+
+def _int_array(values, n):
+    values = [int(v) for v in values]
+    if len(values) != n:
+        raise ValueError(f"expected {n} values, got {len(values)}")
+    return (ctypes.c_int * n)(*values)
 
 
 def _check(status, where):
@@ -299,6 +320,85 @@ def dcnv4_fused_forward_algo(x, w_om, b_om, out, N, H, W, C, G, kh, kw, pad, dil
                                             C, G, kh, kw, pad, dil, dtype, algo,
                                             _stream(stream)),
            "dcnv4_fused_forward_algo")
+
+
+def axial_rope_forward(x, pos, freqs, out, axis_pairs, N, L, M, D, A, pos_images, x_image, x_row,
+                       interleaved, inverse, dtype, stream=None):
+    """C axial_rope_forward (axis_pairs: a sequence of A ints); raises DcnError
+    on a non-OK status."""
+    _check(_load().axial_rope_forward(_ptr(x), _ptr(pos), _ptr(freqs), _ptr(out),
+                                      _int_array(axis_pairs, A), N, L, M, D, A, pos_images,
+                                      x_image, x_row, interleaved, inverse, dtype,
+                                      _stream(stream)),
+           "axial_rope_forward")
+
+
+def axial_rope_backward(x, pos, freqs, grad_out, grad_x, grad_pos, axis_pairs, N, L, M, D, A,
+                        pos_images, x_image, x_row, interleaved, inverse, dtype, stream=None):
+    """C axial_rope_backward; raises DcnError on a non-OK status."""
+    _check(_load().axial_rope_backward(_ptr(x), _ptr(pos), _ptr(freqs), _ptr(grad_out),
+                                       _ptr(grad_x), _ptr(grad_pos), _int_array(axis_pairs, A),
+                                       N, L, M, D, A, pos_images, x_image, x_row, interleaved,
+                                       inverse, dtype, _stream(stream)),
+           "axial_rope_backward")
+
+
+def norm_residual_forward(x, y, scale, gate, post_weight, post_bias, pre_weight, pre_bias, z, h,
+                          N, L, C, flags, eps, dtype, stream=None):
+    """C norm_residual_forward; raises DcnError on a non-OK status."""
+    _check(_load().norm_residual_forward(_ptr(x), _ptr(y), _ptr(scale), _ptr(gate),
+                                         _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight),
+                                         _ptr(pre_bias), _ptr(z), _ptr(h), N, L, C, flags, eps,
+                                         dtype, _stream(stream)),
+           "norm_residual_forward")
+
+
+def norm_residual_backward_workspace_size(N, L, C, gated, dtype):
+    return int(_load().norm_residual_backward_workspace_size(N, L, C, gated, dtype))
+
+
+def norm_residual_backward(y, z, grad_z, grad_h, scale, gate, post_weight, post_bias, pre_weight,
+                           grad_x, grad_y, grad_scale, grad_gate, grad_post_weight,
+                           grad_post_bias, grad_pre_weight, grad_pre_bias, workspace,
+                           workspace_bytes, N, L, C, flags, eps, dtype, stream=None):
+    """C norm_residual_backward; raises DcnError on a non-OK status."""
+    _check(_load().norm_residual_backward(
+        _ptr(y), _ptr(z), _ptr(grad_z), _ptr(grad_h), _ptr(scale), _ptr(gate), _ptr(post_weight),
+        _ptr(post_bias), _ptr(pre_weight), _ptr(grad_x), _ptr(grad_y), _ptr(grad_scale),
+        _ptr(grad_gate), _ptr(grad_post_weight), _ptr(grad_post_bias), _ptr(grad_pre_weight),
+        _ptr(grad_pre_bias), _ptr(workspace), workspace_bytes, N, L, C, flags, eps, dtype,
+        _stream(stream)), "norm_residual_backward")
+
+
+def diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype):
+    return int(_load().diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype))
+
+
+def diff_attn_forward(q, k, v, lam, mask, lengths, out, out2, lse, workspace, workspace_bytes, N,
+                      Lq, Lk, M, Mk, D, Dv, q_image, q_row, k_image, k_row, v_image, v_row, scale,
+                      causal, dtype, stream=None):
+    """C diff_attn_forward; raises DcnError on a non-OK status."""
+    _check(_load().diff_attn_forward(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(mask), _ptr(lengths), _ptr(out), _ptr(out2),
+        _ptr(lse), _ptr(workspace), workspace_bytes, N, Lq, Lk, M, Mk, D, Dv, q_image, q_row,
+        k_image, k_row, v_image, v_row, scale, causal, dtype, _stream(stream)),
+        "diff_attn_forward")
+
+
+def diff_attn_backward_workspace_size(N, Lq, M, dtype):
+    return int(_load().diff_attn_backward_workspace_size(N, Lq, M, dtype))
+
+
+def diff_attn_backward(q, k, v, lam, mask, lengths, out, out2, lse, grad_out, grad_q, grad_k,
+                       grad_v, grad_lam, workspace, workspace_bytes, N, Lq, Lk, M, Mk, D, Dv,
+                       q_image, q_row, k_image, k_row, v_image, v_row, scale, causal, dtype,
+                       stream=None):
+    """C diff_attn_backward; raises DcnError on a non-OK status."""
+    _check(_load().diff_attn_backward(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(mask), _ptr(lengths), _ptr(out), _ptr(out2),
+        _ptr(lse), _ptr(grad_out), _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(grad_lam),
+        _ptr(workspace), workspace_bytes, N, Lq, Lk, M, Mk, D, Dv, q_image, q_row, k_image, k_row,
+        v_image, v_row, scale, causal, dtype, _stream(stream)), "diff_attn_backward")
 
 
 def dcn_output_size(n_in, k, stride, pad, dil):
@@ -548,3 +648,256 @@ def dcnv4_fused(x, w_om, b_om=None, groups=4, kh=3, kw=3, pad=1, dil=1, out=None
     dcnv4_fused_forward_algo(x, w_om, b_om, out, N, H, W, C, groups, kh, kw, pad, dil,
                              dtype_code(x), ALGO_CODES[algo], stream)
     return out
+
+
+# ------------------------------------------------ attention-block operators
+
+def _on_device(t):
+    """A context in which the tensor's device is the current one (launches and
+    the current stream belong to the current device)."""
+    import contextlib
+
+    import torch
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _same_device(first, *rest):
+    _require(first.is_cuda, "tensors must be on a CUDA device")
+    for t in rest:
+        _require(t is None or t.device == first.device, "tensors must be on one CUDA device")
+
+
+def _heads_stride(t, shape, name):
+    """(image, token) strides of a [N, L, ...] tensor whose inner dimensions are dense."""
+    _require(tuple(t.shape) == shape, f"{name} has the wrong shape")
+    inner = 1
+    for size, stride in zip(reversed(shape[2:]), reversed(t.stride()[2:])):
+        _require(size == 1 or stride == inner, f"{name} must be dense in its last dimensions")
+        inner *= size
+    N, L = shape[:2]
+    row = t.stride(1) if L > 1 else inner
+    image = t.stride(0) if N > 1 else max(L, 1) * row
+    _require((row >= inner and image >= 0) or N * L == 0,
+             f"{name} has overlapping tokens or a negative stride")
+    return (image, row) if N * L else (L * inner, inner)
+
+
+def _rope_checks(x, pos, freqs, axis_pairs, inverse, interleaved):
+    import torch
+    _require(x.dim() == 4 and pos.dim() == 3, "expected x [N,L,M,D], pos [N or 1,L,A]")
+    N, L, M, D = x.shape
+    A = pos.shape[2]
+    _require(pos.shape[0] in (1, N) and pos.shape[1] == L, "pos must be [N or 1, L, A]")
+    _require(1 <= A <= 4, "1 to 4 axes")
+    _require(len(axis_pairs) == A, "axis_pairs must hold one count per axis")
+    _require(all(p >= 0 for p in axis_pairs) and 2 * sum(axis_pairs) <= D,
+             "axis_pairs must be non-negative and rotate at most D channels")
+    _require(tuple(freqs.shape) == (sum(axis_pairs),), "freqs must hold one value per pair")
+    _require(pos.dtype == torch.float32 and freqs.dtype == torch.float32,
+             "pos and freqs must be float32")
+    _same_device(x, pos, freqs)
+    _require(pos.is_contiguous() and freqs.is_contiguous(), "pos and freqs must be contiguous")
+    return N, L, M, D, A, _heads_stride(x, (N, L, M, D), "x")
+
+
+def axial_rope(x, pos, freqs, axis_pairs, interleaved=False, inverse=False, out=None,
+               stream=None):
+    """Rotary positions over one to four axes (axial_rope_forward).
+
+    x [N, L, M, D] (heads and channels dense; images and tokens may be strided),
+    pos [N or 1, L, A] float32, freqs [sum(axis_pairs)] float32; axis_pairs:
+    the number of channel pairs each axis turns.  `out` may be x (in place).
+    """
+    import torch
+    N, L, M, D, A, (image, row) = _rope_checks(x, pos, freqs, axis_pairs, inverse, interleaved)
+    code = dtype_code(x)
+    if out is None:
+        out = torch.empty((N, L, M, D), dtype=x.dtype, device=x.device)
+    _require(out.shape == x.shape and out.dtype == x.dtype and out.device == x.device
+             and out.is_contiguous(), "out has the wrong shape, dtype, device or layout")
+    with _on_device(x):
+        axial_rope_forward(x, pos, freqs, out, axis_pairs, N, L, M, D, A, pos.shape[0], image, row,
+                           int(bool(interleaved)), int(bool(inverse)), code, stream)
+    return out
+
+
+def axial_rope_grad(x, pos, freqs, axis_pairs, grad_out, interleaved=False, inverse=False,
+                    need_pos=True, stream=None):
+    """axial_rope_backward: returns (grad_x, grad_pos); grad_pos is None without need_pos."""
+    import torch
+    N, L, M, D, A, (image, row) = _rope_checks(x, pos, freqs, axis_pairs, inverse, interleaved)
+    _require(grad_out.shape == x.shape and grad_out.dtype == x.dtype and grad_out.is_contiguous(),
+             "grad_out has the wrong shape, dtype or layout")
+    _same_device(x, grad_out)
+    code = dtype_code(x)
+    gx = torch.empty((N, L, M, D), dtype=x.dtype, device=x.device)
+    gp = None
+    if need_pos:    # no images: the launch that would fill a shared pos' gradient does not run
+        gp = (torch.empty if N else torch.zeros)(pos.shape, dtype=pos.dtype, device=x.device)
+    with _on_device(x):
+        axial_rope_backward(x, pos, freqs, grad_out, gx, gp, axis_pairs, N, L, M, D, A,
+                            pos.shape[0], image, row, int(bool(interleaved)), int(bool(inverse)),
+                            code, stream)
+    return gx, gp
+
+
+_NORM_FLAGS = {"layer": 0, "rms": DCN_NORM_RMS}
+
+
+def _norm_checks(rows, factors, norm, post, pre):
+    """(N, L, C, flags, dtype code) of dense [N, L, C] tensors and their factors."""
+    t = rows[0]
+    _require(t.dim() == 3, "expected [N, L, C] tensors")
+    N, L, C = t.shape
+    _require(norm in _NORM_FLAGS, f"norm must be one of {sorted(_NORM_FLAGS)}")
+    _same_device(*rows, *(f for f, _ in factors))
+    for r in rows:
+        _require(r is None or (r.shape == t.shape and r.dtype == t.dtype and r.is_contiguous()),
+                 "row tensors must be contiguous [N, L, C] of one dtype")
+    for f, gated in factors:
+        shape = (N, C) if gated else (C,)
+        _require(f is None or (tuple(f.shape) == shape and f.dtype == t.dtype
+                               and f.is_contiguous()),
+                 "factors must be contiguous [C] (gate: [N, C]) of the rows' dtype")
+    flags = _NORM_FLAGS[norm] | (DCN_NORM_POST if post else 0) | (DCN_NORM_PRE if pre else 0)
+    return N, L, C, flags, dtype_code(t)
+
+
+def norm_residual(x, y, scale=None, gate=None, post_weight=None, post_bias=None, pre_weight=None,
+                  pre_bias=None, norm="layer", post=True, pre=True, eps=1e-6, out=None,
+                  stream=None):
+    """norm_residual_forward: returns (z, h), the joined residual stream and the
+    next block's normed input (None without pre).
+
+    z = x + scale * gate * (norm(y) * post_weight + post_bias), h = norm(z) *
+    pre_weight + pre_bias; x, y [N, L, C], gate [N, C], the other factors [C].
+    norm: "layer" or "rms"; post / pre switch the two norms.  out=x joins in place.
+    """
+    import torch
+    N, L, C, flags, code = _norm_checks(
+        (x, y), ((scale, False), (gate, True), (post_weight, False), (post_bias, False),
+                 (pre_weight, False), (pre_bias, False)), norm, post, pre)
+    z = torch.empty_like(x) if out is None else out
+    _require(z.shape == x.shape and z.dtype == x.dtype and z.device == x.device
+             and z.is_contiguous(), "out has the wrong shape, dtype, device or layout")
+    h = torch.empty_like(x) if pre else None
+    with _on_device(x):
+        norm_residual_forward(x, y, scale, gate, post_weight, post_bias, pre_weight, pre_bias, z,
+                              h, N, L, C, flags, eps, code, stream)
+    return z, h
+
+
+def norm_residual_grad(y, z, grad_z, grad_h=None, scale=None, gate=None, post_weight=None,
+                       post_bias=None, pre_weight=None, pre_bias=None, norm="layer", post=True,
+                       pre=True, eps=1e-6, workspace=None, stream=None):
+    """norm_residual_backward: returns (grad_x, grad_y, grad_scale, grad_gate,
+    grad_post_weight, grad_post_bias, grad_pre_weight, grad_pre_bias), None for
+    the factors that are None.  z is norm_residual's first output."""
+    import torch
+    N, L, C, flags, code = _norm_checks(
+        (y, z, grad_z, grad_h),
+        ((scale, False), (gate, True), (post_weight, False), (post_bias, False),
+         (pre_weight, False), (pre_bias, False)), norm, post, pre)
+    _require((grad_h is not None) == bool(pre), "grad_h belongs to pre=True")
+
+    def like(f):
+        return None if f is None else torch.empty_like(f)
+
+    gx, gy = torch.empty_like(y), torch.empty_like(y)
+    gs, gg, gpw, gpb = like(scale), like(gate), like(post_weight), like(post_bias)
+    gqw, gqb = like(pre_weight), like(pre_bias)
+    with _on_device(y):
+        need = norm_residual_backward_workspace_size(N, L, C, 0 if gate is None else 1, code)
+        if need < 0:
+            raise DcnError(need, "norm_residual_backward_workspace_size")
+        ws, ws_bytes = _workspace(need, y.device, workspace)
+        norm_residual_backward(y, z, grad_z, grad_h, scale, gate, post_weight, post_bias,
+                               pre_weight, gx, gy, gs, gg, gpw, gpb, gqw, gqb, ws, ws_bytes, N, L,
+                               C, flags, eps, code, stream)
+    return gx, gy, gs, gg, gpw, gpb, gqw, gqb
+
+
+def _attn_checks(q, k, v, lam, mask, lengths):
+    import torch
+    _require(q.dim() == 5 and k.dim() == 5 and v.dim() == 4,
+             "expected q [N,Lq,M,2,D], k [N,Lk,Mk,2,D], v [N,Lk,Mk,Dv]")
+    N, Lq, M, _, D = q.shape
+    Lk, Mk, Dv = v.shape[1:]
+    _require(Mk > 0 and M % Mk == 0, "the heads must be a multiple of the key / value heads")
+    _same_device(q, k, v, lam, mask, lengths)
+    for t in (k, v, lam):
+        _require(t.dtype == q.dtype, "mixed dtypes")
+    strides = (_heads_stride(q, (N, Lq, M, 2, D), "q") + _heads_stride(k, (N, Lk, Mk, 2, D), "k") +
+               _heads_stride(v, (N, Lk, Mk, Dv), "v"))
+    _require(tuple(lam.shape) == (M,) and lam.is_contiguous(), "lam must be a contiguous [M]")
+    if mask is not None:
+        _require(tuple(mask.shape) == (N, Lk) and mask.is_contiguous()
+                 and mask.dtype in (torch.bool, torch.uint8), "mask must be [N, Lk] bool or uint8")
+    _require(lengths is None or (tuple(lengths.shape) == (N,) and lengths.dtype == torch.int32
+                                 and lengths.is_contiguous()), "lengths must be [N] int32")
+    return (N, Lq, Lk, M, Mk, D, Dv), strides
+
+
+def diff_attn(q, k, v, lam, mask=None, lengths=None, causal=False, scale=None, save=False,
+              out=None, workspace=None, stream=None):
+    """diff_attn_forward: out [N, Lq, M, Dv] of differential attention,
+    (softmax(scale q_0 k_0^T) - lam softmax(scale q_1 k_1^T)) v.
+
+    q [N, Lq, M, 2, D], k [N, Lk, Mk, 2, D], v [N, Lk, Mk, Dv] (images and
+    tokens may be strided), lam [M]; mask [N, Lk], true where a key is hidden;
+    lengths [N] int32, the keys in use; causal: the tokens are the last Lq of
+    those.  scale: 1 / sqrt(D) unless given.  save=True returns (out, saved)
+    with what diff_attn_grad needs.
+    """
+    import torch
+    (N, Lq, Lk, M, Mk, D, Dv), strides = _attn_checks(q, k, v, lam, mask, lengths)
+    code = dtype_code(q)
+    if out is None:
+        out = torch.empty((N, Lq, M, Dv), dtype=q.dtype, device=q.device)
+    _require(tuple(out.shape) == (N, Lq, M, Dv) and out.dtype == q.dtype
+             and out.device == q.device and out.is_contiguous(),
+             "out has the wrong shape, dtype, device or layout")
+    out2 = lse = None
+    if save:
+        out2 = torch.empty((N, Lq, M, Dv), dtype=q.dtype, device=q.device)
+        lse = torch.empty((N, M, 2, Lq), dtype=torch.float32, device=q.device)
+    with _on_device(q):
+        need = diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, code)
+        if need < 0:
+            raise DcnError(need, "diff_attn_forward_workspace_size")
+        ws, ws_bytes = _workspace(need, q.device, workspace)
+        diff_attn_forward(q, k, v, lam, mask, lengths, out, out2, lse, ws, ws_bytes, N, Lq, Lk, M,
+                          Mk, D, Dv, *strides, D ** -0.5 if scale is None else scale,
+                          int(bool(causal)), code, stream)
+    return (out, (out2, lse)) if save else out
+
+
+def diff_attn_grad(q, k, v, lam, out, saved, grad_out, mask=None, lengths=None, causal=False,
+                   scale=None, workspace=None, stream=None):
+    """diff_attn_backward: returns (grad_q, grad_k, grad_v, grad_lam), dense;
+    out, saved: what diff_attn(..., save=True) returned for these inputs."""
+    import torch
+    (N, Lq, Lk, M, Mk, D, Dv), strides = _attn_checks(q, k, v, lam, mask, lengths)
+    code = dtype_code(q)
+    out2, lse = saved
+    _same_device(q, out, out2, lse, grad_out)
+    for t in (out, out2, grad_out):
+        _require(tuple(t.shape) == (N, Lq, M, Dv) and t.dtype == q.dtype and t.is_contiguous(),
+                 "out, saved and grad_out must be contiguous [N, Lq, M, Dv] of q's dtype")
+    _require(tuple(lse.shape) == (N, M, 2, Lq) and lse.dtype == torch.float32
+             and lse.is_contiguous(), "saved must be diff_attn's")
+    gq = torch.empty((N, Lq, M, 2, D), dtype=q.dtype, device=q.device)
+    gk = torch.empty((N, Lk, Mk, 2, D), dtype=q.dtype, device=q.device)
+    gv = torch.empty((N, Lk, Mk, Dv), dtype=q.dtype, device=q.device)
+    gl = torch.empty_like(lam)
+    with _on_device(q):
+        need = diff_attn_backward_workspace_size(N, Lq, M, code)
+        if need < 0:
+            raise DcnError(need, "diff_attn_backward_workspace_size")
+        ws, ws_bytes = _workspace(need, q.device, workspace)
+        diff_attn_backward(q, k, v, lam, mask, lengths, out, out2, lse, grad_out, gq, gk, gv, gl,
+                           ws, ws_bytes, N, Lq, Lk, M, Mk, D, Dv, *strides,
+                           D ** -0.5 if scale is None else scale, int(bool(causal)), code, stream)
+    return gq, gk, gv, gl

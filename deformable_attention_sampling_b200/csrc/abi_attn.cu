@@ -1,0 +1,393 @@
+// C interface of libdcn_b200.so: diff_attn_forward, diff_attn_backward and
+// their workspace sizes.
+#include "abi_common.cuh"
+#include "diff_attn.cuh"
+
+using namespace dcnb_abi;
+
+namespace {
+
+struct AttnPlan {
+    int bq;            // packed rows of a tile
+    int tiles;         // row tiles of a key / value head
+    int splits;        // key ranges a tile is split into
+};
+
+// Row tile and key splits.  Few rows (a serving step) take the 16-row tile;
+// the keys are split when the tiles alone leave most multiprocessors idle, so
+// that about two blocks a multiprocessor run, each with at least two key
+// tiles (a shorter range costs more in its join than it saves).
+AttnPlan attn_plan(int N, int Lq, int Lk, int M, int Mk) {
+    AttnPlan p;
+    const long long rows = (long long)Lq * (M / Mk);
+    p.bq = rows <= 16 ? 16 : 64;
+    p.tiles = (int)((rows + p.bq - 1) / p.bq);
+    const long long blocks = (long long)p.tiles * N * Mk;
+    const int sms = sm_count();
+    const int key_tiles = (Lk + dcnb::kAttnKeys - 1) / dcnb::kAttnKeys;
+    long long s = blocks < sms ? (2LL * sms + blocks - 1) / std::max(blocks, 1LL) : 1;
+    s = std::min(s, (long long)key_tiles / 2);
+    p.splits = (int)std::max(1LL, std::min(s, (long long)dcnb::kAttnMaxSplits));
+    return p;
+}
+
+template <typename T, int BQ>
+const void* fwd_kernel_ct(int ct) {
+    switch (ct) {
+        case 2: return (const void*)dcnb::diff_attn_kernel<T, BQ, 2>;
+        case 4: return (const void*)dcnb::diff_attn_kernel<T, BQ, 4>;
+        case 8: return (const void*)dcnb::diff_attn_kernel<T, BQ, 8>;
+        case 16: return (const void*)dcnb::diff_attn_kernel<T, BQ, 16>;
+        default: return nullptr;
+    }
+}
+
+template <typename T>
+const void* fwd_kernel(int bq, int ct) {
+    return bq == 16 ? fwd_kernel_ct<T, 16>(ct) : fwd_kernel_ct<T, 64>(ct);
+}
+
+// Columns a thread of 16 owns of a head size: 2, 4, 8 or 16.
+int columns(int d) {
+    int c = 2;
+    while (16 * c < d) c <<= 1;
+    return c;
+}
+
+// The gradient kernels' tile: 64 where shared memory holds it (heads up to 64
+// and values up to 128 channels), else 32.
+int bwd_tile(int cd, int ct) { return cd <= 4 && ct <= 8 ? 64 : 32; }
+
+template <typename T, int BT, int CD>
+void bwd_kernels_ct(int ct, const void** dq, const void** dkv) {
+    switch (ct) {
+        case 2:
+            *dq = (const void*)dcnb::diff_attn_dq_kernel<T, BT, CD, 2>;
+            *dkv = (const void*)dcnb::diff_attn_dkv_kernel<T, BT, CD, 2>;
+            break;
+        case 4:
+            *dq = (const void*)dcnb::diff_attn_dq_kernel<T, BT, CD, 4>;
+            *dkv = (const void*)dcnb::diff_attn_dkv_kernel<T, BT, CD, 4>;
+            break;
+        case 8:
+            *dq = (const void*)dcnb::diff_attn_dq_kernel<T, BT, CD, 8>;
+            *dkv = (const void*)dcnb::diff_attn_dkv_kernel<T, BT, CD, 8>;
+            break;
+        case 16:
+            if constexpr (BT == 32) {
+                *dq = (const void*)dcnb::diff_attn_dq_kernel<T, BT, CD, 16>;
+                *dkv = (const void*)dcnb::diff_attn_dkv_kernel<T, BT, CD, 16>;
+            }
+            break;
+        default: break;
+    }
+}
+
+template <typename T>
+void bwd_kernels(int cd, int ct, const void** dq, const void** dkv) {
+    const bool big = bwd_tile(cd, ct) == 64;
+    switch (cd) {
+        case 2:
+            if (big) bwd_kernels_ct<T, 64, 2>(ct, dq, dkv);
+            else bwd_kernels_ct<T, 32, 2>(16, dq, dkv);
+            break;
+        case 4:
+            if (big) bwd_kernels_ct<T, 64, 4>(ct, dq, dkv);
+            else bwd_kernels_ct<T, 32, 4>(16, dq, dkv);
+            break;
+        case 8: bwd_kernels_ct<T, 32, 8>(ct, dq, dkv); break;
+        default: break;
+    }
+}
+
+// Checks shared by both directions; fills the geometry.  `strides`: image and
+// row strides of q, k, v.
+int attn_setup(dcnb::AttnArgs* a, const void* q, const void* k, const void* v, const void* lam,
+               const unsigned char* mask, const int* lengths, int N, int Lq, int Lk, int M, int Mk,
+               int D, int Dv, long long q_image, long long q_row, long long k_image,
+               long long k_row, long long v_image, long long v_row, float scale, int causal,
+               int dtype) {
+    const int es = elem_bytes(dtype);
+    if (es == 0 || N < 0 || Lq < 0 || Lk < 0 || M <= 0 || Mk <= 0 || M % Mk != 0 || D <= 0 ||
+        Dv <= 0 || (causal != 0 && causal != 1) || !std::isfinite(scale) || q_image < 0 ||
+        k_image < 0 || v_image < 0)
+        return DCN_ERR_INVALID_ARG;
+    if (D > dcnb::kAttnMaxD || Dv > dcnb::kAttnMaxDv || M > 65535 ||
+        (long long)N * Mk > 65535 || (long long)Lq * (M / Mk) > kInt31 - 65536 ||
+        (long long)Lk > kInt31 - 65536 || (long long)Lq + Lk > kInt31 - 65536)
+        return DCN_ERR_UNSUPPORTED;
+    if (q_row < (long long)M * 2 * D || k_row < (long long)Mk * 2 * D ||
+        v_row < (long long)Mk * Dv)
+        return DCN_ERR_INVALID_ARG;
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->lam = lam;
+    a->mask = mask;
+    a->lengths = lengths;
+    a->N = N;
+    a->Lq = Lq;
+    a->Lk = Lk;
+    a->M = M;
+    a->Mk = Mk;
+    a->G = M / Mk;
+    a->D = D;
+    a->Dv = Dv;
+    a->rows = Lq * a->G;
+    a->splits = 1;
+    a->causal = causal;
+    a->scale = scale;
+    a->scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    a->q_image = q_image;
+    a->q_row = q_row;
+    a->k_image = k_image;
+    a->k_row = k_row;
+    a->v_image = v_image;
+    a->v_row = v_row;
+    a->div_G = make_div((uint32_t)a->G);
+    a->div_Mk = make_div((uint32_t)Mk);
+    const uintptr_t bits = (uintptr_t)q | (uintptr_t)k | (uintptr_t)v;
+    const long long strides = q_image | q_row | k_image | k_row | v_image | v_row;
+    a->vec4 = D % 4 == 0 && Dv % 4 == 0 && strides % 4 == 0 && bits % (uintptr_t)(4 * es) == 0;
+    return DCN_OK;
+}
+
+// Pointers of a non-empty call: present, aligned.
+int attn_pointers(const dcnb::AttnArgs& a, int es) {
+    if (!a.q || !a.lam || (a.Lk > 0 && (!a.k || !a.v))) return DCN_ERR_INVALID_ARG;
+    if (((uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.lam) % es != 0 ||
+        (uintptr_t)a.lengths % 4 != 0)
+        return DCN_ERR_MISALIGNED;
+    return DCN_OK;
+}
+
+struct Span {
+    const void* p;
+    long long bytes;
+};
+
+bool clash(const Span& a, const Span& b) {
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && overlaps(a.p, a.bytes, b.p, b.bytes);
+}
+
+long long strided_bytes(int N, long long image, int L, long long row, long long inner, int es) {
+    return N > 0 && L > 0 ? ((N - 1) * image + (L - 1) * row + inner) * es : 0;
+}
+
+constexpr int kInputs = 6;
+
+void input_spans(const dcnb::AttnArgs& a, int es, Span* s) {
+    s[0] = {a.q, strided_bytes(a.N, a.q_image, a.Lq, a.q_row, 2LL * a.M * a.D, es)};
+    s[1] = {a.k, strided_bytes(a.N, a.k_image, a.Lk, a.k_row, 2LL * a.Mk * a.D, es)};
+    s[2] = {a.v, strided_bytes(a.N, a.v_image, a.Lk, a.v_row, (long long)a.Mk * a.Dv, es)};
+    s[3] = {a.lam, (long long)a.M * es};
+    s[4] = {a.mask, (long long)a.N * a.Lk};
+    s[5] = {a.lengths, 4LL * a.N};
+}
+
+bool any_clash(const Span* outs, int n_out, const Span* ins, int n_in) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (clash(outs[i], ins[j])) return true;
+        for (int j = 0; j < i; ++j)
+            if (clash(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+// A grid whose x counts row or key tiles and y the (image, key / value head)
+// pairs, z the splits.
+int launch_attn(const void* fn, const dcnb::AttnArgs& a, dim3 grid, int threads, int smem,
+                void* stream) {
+    if (wave_size(fn, threads, smem) <= 0) {
+        g_last_cuda_error = (int)cudaGetLastError();
+        return DCN_ERR_CUDA;
+    }
+    void* params[] = {const_cast<dcnb::AttnArgs*>(&a)};
+    const cudaError_t err =
+        cudaLaunchKernel(fn, grid, dim3(threads), params, (size_t)smem, (cudaStream_t)stream);
+    if (err != cudaSuccess) {
+        g_last_cuda_error = (int)err;
+        (void)cudaGetLastError();
+        return DCN_ERR_CUDA;
+    }
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return DCN_OK;
+}
+
+template <typename T>
+const void* join_kernel() { return (const void*)dcnb::diff_attn_join_kernel<T>; }
+
+}  // namespace
+
+extern "C" {
+
+long long diff_attn_forward_workspace_size(int N, int Lq, int Lk, int M, int Mk, int D, int Dv,
+                                           int dtype) {
+    dcnb::AttnArgs a = {};
+    const long long qd = 2LL * M * D, kd = 2LL * Mk * D, vd = (long long)Mk * Dv;
+    const int st = attn_setup(&a, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, N, Lq, Lk,
+                              M, Mk, D, Dv, 0, qd, 0, kd, 0, vd, 1.f, 0, dtype);
+    if (st != DCN_OK) return st;
+    if (N == 0 || Lq == 0) return 0;
+    const AttnPlan p = attn_plan(N, Lq, Lk, M, Mk);
+    if (p.splits == 1) return 0;
+    return (long long)p.splits * N * M * Lq * 2 * (2 + (long long)Dv) * 4;
+}
+
+int diff_attn_forward(const void* q, const void* k, const void* v, const void* lambda,
+                      const unsigned char* mask, const int* lengths, void* out, void* out2,
+                      float* lse, void* workspace, long long workspace_bytes, int N, int Lq, int Lk,
+                      int M, int Mk, int D, int Dv, long long q_image, long long q_row,
+                      long long k_image, long long k_row, long long v_image, long long v_row,
+                      float scale, int causal, int dtype, void* stream) {
+    dcnb::AttnArgs a = {};
+    int rc = attn_setup(&a, q, k, v, lambda, mask, lengths, N, Lq, Lk, M, Mk, D, Dv, q_image, q_row,
+                        k_image, k_row, v_image, v_row, scale, causal, dtype);
+    if (rc != DCN_OK) return rc;
+    if (N == 0 || Lq == 0) return DCN_OK;
+    const int es = elem_bytes(dtype);
+    if ((rc = attn_pointers(a, es)) != DCN_OK) return rc;
+    if (!out || (out2 == nullptr) != (lse == nullptr)) return DCN_ERR_INVALID_ARG;
+    if (((uintptr_t)out | (uintptr_t)out2) % es != 0 || (uintptr_t)lse % 4 != 0 ||
+        (uintptr_t)workspace % 16 != 0)
+        return DCN_ERR_MISALIGNED;
+    const AttnPlan p = attn_plan(N, Lq, Lk, M, Mk);
+    const long long need = diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return DCN_ERR_INVALID_ARG;
+    const long long ob = (long long)N * Lq * M * Dv * es;
+    Span ins[kInputs];
+    input_spans(a, es, ins);
+    const Span outs[] = {{out, ob}, {out2, ob}, {lse, (long long)N * M * 2 * Lq * 4},
+                         {workspace, need}};
+    if (any_clash(outs, 4, ins, kInputs)) return DCN_ERR_INVALID_ARG;
+    a.out = out;
+    a.out2 = out2;
+    a.lse = lse;
+    a.splits = p.splits;
+    const long long rows_total = (long long)N * M * Lq;
+    if (p.splits > 1) {
+        a.part_o = static_cast<float*>(workspace);
+        a.part_ml = a.part_o + (long long)p.splits * rows_total * 2 * Dv;
+    }
+    const int ct = columns(Dv);
+    const void* fn = nullptr;
+    const void* join = nullptr;
+    switch (dtype) {
+        case DCN_F32: fn = fwd_kernel<float>(p.bq, ct); join = join_kernel<float>(); break;
+        case DCN_F16: fn = fwd_kernel<__half>(p.bq, ct); join = join_kernel<__half>(); break;
+        case DCN_BF16:
+            fn = fwd_kernel<__nv_bfloat16>(p.bq, ct);
+            join = join_kernel<__nv_bfloat16>();
+            break;
+        default: break;
+    }
+    if (!fn) return DCN_ERR_UNSUPPORTED;
+    rc = launch_attn(fn, a, dim3(p.tiles, N * Mk, p.splits), dcnb::kAttnThreads,
+                     dcnb::attn_fwd_smem(p.bq, D, ct), stream);
+    if (rc != DCN_OK || p.splits == 1) return rc;
+    return launch_attn(join, a, dim3((unsigned)((rows_total + 7) / 8)), 256, 0, stream);
+}
+
+long long diff_attn_backward_workspace_size(int N, int Lq, int M, int dtype) {
+    if (elem_bytes(dtype) == 0 || N < 0 || Lq < 0 || M <= 0) return DCN_ERR_INVALID_ARG;
+    return (long long)N * M * 2 * Lq * 4;
+}
+
+int diff_attn_backward(const void* q, const void* k, const void* v, const void* lambda,
+                       const unsigned char* mask, const int* lengths, const void* out,
+                       const void* out2, const float* lse, const void* grad_out, void* grad_q,
+                       void* grad_k, void* grad_v, void* grad_lambda, void* workspace,
+                       long long workspace_bytes, int N, int Lq, int Lk, int M, int Mk, int D,
+                       int Dv, long long q_image, long long q_row, long long k_image,
+                       long long k_row, long long v_image, long long v_row, float scale, int causal,
+                       int dtype, void* stream) {
+    dcnb::AttnArgs a = {};
+    int rc = attn_setup(&a, q, k, v, lambda, mask, lengths, N, Lq, Lk, M, Mk, D, Dv, q_image, q_row,
+                        k_image, k_row, v_image, v_row, scale, causal, dtype);
+    if (rc != DCN_OK) return rc;
+    const int es = elem_bytes(dtype);
+    const long long tokens = (long long)N * Lq, keys = (long long)N * Lk;
+    if (!grad_lambda) return DCN_ERR_INVALID_ARG;
+    if (tokens > 0) {
+        if ((rc = attn_pointers(a, es)) != DCN_OK) return rc;
+        if (!out || !out2 || !lse || !grad_out || !grad_q || !workspace) return DCN_ERR_INVALID_ARG;
+    }
+    if (keys > 0 && (!grad_k || !grad_v)) return DCN_ERR_INVALID_ARG;
+    if (((uintptr_t)out | (uintptr_t)out2 | (uintptr_t)grad_out | (uintptr_t)grad_q |
+         (uintptr_t)grad_k | (uintptr_t)grad_v | (uintptr_t)grad_lambda) % es != 0 ||
+        ((uintptr_t)lse | (uintptr_t)lengths) % 4 != 0 || (uintptr_t)workspace % 16 != 0)
+        return DCN_ERR_MISALIGNED;
+    const long long need = diff_attn_backward_workspace_size(N, Lq, M, dtype);
+    if (workspace_bytes < need) return DCN_ERR_INVALID_ARG;
+    const long long ob = tokens * M * Dv * es, sb = tokens * M * 2 * 4;
+    Span ins[kInputs + 4];
+    input_spans(a, es, ins);
+    ins[kInputs] = {out, ob};
+    ins[kInputs + 1] = {out2, ob};
+    ins[kInputs + 2] = {lse, sb};
+    ins[kInputs + 3] = {grad_out, ob};
+    const Span outs[] = {{grad_q, tokens * M * 2 * D * es}, {grad_k, keys * Mk * 2 * D * es},
+                         {grad_v, keys * Mk * Dv * es}, {grad_lambda, (long long)M * es},
+                         {workspace, need}};
+    if (any_clash(outs, 5, ins, kInputs + 4)) return DCN_ERR_INVALID_ARG;
+    a.vec4 = a.vec4 && (uintptr_t)grad_out % (uintptr_t)(4 * es) == 0;
+    a.go = grad_out;
+    a.lse = const_cast<float*>(lse);
+    a.delta = static_cast<const float*>(workspace);
+    a.gq = grad_q;
+    a.gk = grad_k;
+    a.gv = grad_v;
+
+    const int cd = columns(D), ct = columns(Dv), bt = bwd_tile(cd, ct);
+    const void *dq = nullptr, *dkv = nullptr, *delta = nullptr, *glam = nullptr;
+    switch (dtype) {
+        case DCN_F32:
+            bwd_kernels<float>(cd, ct, &dq, &dkv);
+            delta = (const void*)dcnb::diff_attn_delta_kernel<float>;
+            glam = (const void*)dcnb::diff_attn_glam_kernel<float>;
+            break;
+        case DCN_F16:
+            bwd_kernels<__half>(cd, ct, &dq, &dkv);
+            delta = (const void*)dcnb::diff_attn_delta_kernel<__half>;
+            glam = (const void*)dcnb::diff_attn_glam_kernel<__half>;
+            break;
+        case DCN_BF16:
+            bwd_kernels<__nv_bfloat16>(cd, ct, &dq, &dkv);
+            delta = (const void*)dcnb::diff_attn_delta_kernel<__nv_bfloat16>;
+            glam = (const void*)dcnb::diff_attn_glam_kernel<__nv_bfloat16>;
+            break;
+        default: break;
+    }
+    if (!dq || !dkv) return DCN_ERR_UNSUPPORTED;
+    dcnb::AttnDeltaArgs d = {};
+    d.out = out;
+    d.out2 = out2;
+    d.go = grad_out;
+    d.lam = lambda;
+    d.delta = static_cast<float*>(workspace);
+    d.glam = grad_lambda;
+    d.N = N;
+    d.Lq = Lq;
+    d.M = M;
+    d.Dv = Dv;
+    if (tokens > 0) {
+        rc = launch_grid(delta, d, (int)((tokens * M + 7) / 8), 256, 0, stream);
+        if (rc != DCN_OK) return rc;
+    }
+    rc = launch_grid(glam, d, M, 1024, 0, stream);       // zeros for an empty batch
+    if (rc != DCN_OK) return rc;
+    const int use_ct = bt == 32 && cd <= 4 ? 16 : ct;
+    const int smem = dcnb::attn_bwd_smem(bt, cd, use_ct);
+    if (tokens > 0) {
+        rc = launch_attn(dq, a, dim3((a.rows + bt - 1) / bt, N * Mk), dcnb::kAttnThreads, smem,
+                         stream);
+        if (rc != DCN_OK) return rc;
+    }
+    if (keys > 0)
+        rc = launch_attn(dkv, a, dim3((Lk + bt - 1) / bt, N * Mk), dcnb::kAttnThreads, smem,
+                         stream);
+    return rc;
+}
+
+}  // extern "C"

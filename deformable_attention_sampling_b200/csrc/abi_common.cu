@@ -38,7 +38,8 @@ struct GridCacheEntry {
     int carveout;
 };
 std::mutex g_grid_mutex;
-GridCacheEntry g_grid_cache[64];
+constexpr int kGridCacheSize = 512;
+GridCacheEntry g_grid_cache[kGridCacheSize];
 int g_grid_cache_n = 0;
 
 }  // namespace
@@ -92,7 +93,7 @@ int wave_size(const void* fn, int threads, int smem) {
         (void)cudaGetLastError();
         carve = -1;
     }
-    if (g_grid_cache_n < 64)
+    if (g_grid_cache_n < kGridCacheSize)
         g_grid_cache[g_grid_cache_n++] = {fn, device, threads, smem, per_sm, sms, carve};
     return per_sm * sms;
 }

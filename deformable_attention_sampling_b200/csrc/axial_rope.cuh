@@ -1,0 +1,217 @@
+// Rotary positions over one to four axes, forward and gradient (sm_100a).
+//
+// Pair i < R of a head's channels turns by th_i = pos[axis(i)] * freqs[i]:
+//   (a, b) -> (a cos th - b sin th, a sin th + b cos th),
+// with (a, b) channels (2i, 2i + 1) (interleaved) or (i, i + R) (halves);
+// channels from 2R on pass through.  The gradient of the channels is the turn
+// by -th; that of a position sums, over the heads and the axis's pairs,
+//   freqs[i] * (gb * a' - ga * b'),   (a', b') the turned pair.
+//
+// Bound: one read of x (and grad_out) and one write, so HBM for many tokens
+// and launch latency for few.  The angles are the only other work: R per
+// token, shared by its M heads.  A team of `tpt` lanes (a power of two up to a
+// warp) owns one token: it forms the token's R (cos, sin) pairs in shared
+// memory once and then turns the token's heads with 16-byte accesses.
+//
+// Angles: the product is formed in float64 as a count of turns and reduced by
+// rint there, because float32 holds a position of 1e5 times a frequency of 1
+// only to 0.004 rad; what is left (|t| <= 1/2 turn) is exact enough in float32.
+#pragma once
+
+#include "common.cuh"
+
+namespace dcnb {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxPairs = 256;
+constexpr int kRopeMaxAxes = 4;
+
+struct RopeArgs {
+    const void* x;
+    const float* pos;
+    const float* freqs;
+    const void* go;            // gradient kernel: gradient of the turned channels
+    void* out;                 // turned channels, or their gradient with respect to x
+    float* grad_pos;           // gradient kernel, or null
+    int L, M, D, R, A;
+    int pair_end[kRopeMaxAxes];   // first pair past axis a
+    long long x_image, x_row;  // elements between images / tokens of x
+    long long units;           // tokens that teams own
+    int images;                // images a unit spans (positions shared by the batch), else 1
+    int shared_pos;            // 1: pos has one image for all
+    int tpt;                   // lanes per token, a power of two
+    int tasks;                 // vector tasks per head
+    int total_tasks;           // M * tasks
+    FastDiv div_tasks, div_L;
+    float sign;                // -1: turn backwards
+};
+
+// VB bytes, cached normally: x may be the output itself (in place), so the
+// read-only path is not used.
+template <int VB>
+__device__ __forceinline__ void ld_words(const void* p, uint32_t* w) {
+    if constexpr (VB == 16) {
+        const uint4 v = *static_cast<const uint4*>(p);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (VB == 8) {
+        const uint2 v = *static_cast<const uint2*>(p);
+        w[0] = v.x; w[1] = v.y;
+    } else if constexpr (VB == 4) {
+        w[0] = *static_cast<const uint32_t*>(p);
+    } else {
+        w[0] = *static_cast<const unsigned short*>(p);
+    }
+}
+
+template <int VB>
+__device__ __forceinline__ void st_words(void* p, const uint32_t* w) {
+    if constexpr (VB == 16) *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (VB == 8) *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (VB == 4) *static_cast<uint32_t*>(p) = w[0];
+    else *static_cast<unsigned short*>(p) = (unsigned short)w[0];
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void ld_f32(const T* p, float* f) {
+    uint32_t w[(V * (int)sizeof(T) + 3) / 4];
+    ld_words<V * (int)sizeof(T)>(p, w);
+    widen<T, V>(w, f);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void st_f32(T* p, const float* f) {
+    uint32_t w[(V * (int)sizeof(T) + 3) / 4];
+    narrow<T, V>(f, w);
+    st_words<V * (int)sizeof(T)>(p, w);
+}
+
+// V elements per access.  INTER with V > 1: a task is one vector of V channels
+// (V / 2 pairs, or V channels that pass).  Halves, or V = 1: a task is V pairs
+// in two vectors, or one vector that passes.
+template <typename T, int V, bool INTER, bool GRAD>
+__global__ void __launch_bounds__(kRopeThreads) axial_rope_kernel(const RopeArgs a) {
+    extern __shared__ float2 rope_turns[];       // [teams][R] (cos, sin)
+    const int tpt = a.tpt;
+    const int team = threadIdx.x / tpt, lane = threadIdx.x & (tpt - 1);
+    const long long unit = (long long)blockIdx.x * (kRopeThreads / tpt) + team;
+    const bool live = unit < a.units;
+    float2* turns = rope_turns + team * a.R;
+    const uint32_t u = live ? (uint32_t)unit : 0u;
+    const uint32_t img = a.images > 1 ? 0u : a.div_L.div(u);
+    const uint32_t l = a.images > 1 ? u : u - img * (uint32_t)a.L;
+    const long long prow = a.shared_pos ? (long long)l : (long long)img * a.L + l;
+    if (live) {
+        for (int i = lane; i < a.R; i += tpt) {
+            int ax = 0;
+            while (ax + 1 < a.A && i >= a.pair_end[ax]) ++ax;
+            double t = (double)a.pos[prow * a.A + ax] * (double)a.freqs[i] *
+                       0.15915494309189533576888376337251436;
+            t -= rint(t);
+            float s, c;
+            sincospif(2.0f * (float)t, &s, &c);
+            turns[i] = make_float2(c, s * a.sign);
+        }
+    }
+    __syncwarp();
+    float acc[kRopeMaxAxes] = {0.f, 0.f, 0.f, 0.f};
+    constexpr bool VINTER = INTER && V > 1;
+    const bool want_pos = GRAD && a.grad_pos != nullptr;
+    if (live) {
+        for (int n = 0; n < a.images; ++n) {
+            const long long token = ((long long)img + n) * a.L + l;
+            const T* x = static_cast<const T*>(a.x) + ((long long)img + n) * a.x_image +
+                         (long long)l * a.x_row;
+            const long long base = token * ((long long)a.M * a.D);
+            const T* src = GRAD ? static_cast<const T*>(a.go) + base : x;
+            T* out = static_cast<T*>(a.out) + base;
+#pragma unroll 2
+            for (int t = lane; t < a.total_tasks; t += tpt) {
+                const int m = (int)a.div_tasks.div((uint32_t)t);
+                const int j = t - m * a.tasks;
+                const int head = m * a.D;
+                if constexpr (VINTER) {
+                    const int c = j * V;
+                    float f[V], r[V];
+                    ld_f32<T, V>(src + head + c, f);
+                    if (c < 2 * a.R) {
+                        float xv[V];
+                        if (want_pos) ld_f32<T, V>(x + head + c, xv);
+#pragma unroll
+                        for (int e = 0; e < V; e += 2) {
+                            const int i = (c + e) >> 1;
+                            const float2 cs = turns[i];
+                            // GRAD: the turn by -th of the gradient
+                            const float s = GRAD ? -cs.y : cs.y;
+                            r[e] = f[e] * cs.x - f[e + 1] * s;
+                            r[e + 1] = f[e] * s + f[e + 1] * cs.x;
+                            if (want_pos) {
+                                const float oa = xv[e] * cs.x - xv[e + 1] * cs.y;
+                                const float ob = xv[e] * cs.y + xv[e + 1] * cs.x;
+                                const float d = a.freqs[i] * (f[e + 1] * oa - f[e] * ob);
+                                int ax = 0;
+                                while (ax + 1 < a.A && i >= a.pair_end[ax]) ++ax;
+#pragma unroll
+                                for (int k = 0; k < kRopeMaxAxes; ++k) acc[k] += k == ax ? d : 0.f;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) r[e] = f[e];
+                    }
+                    st_f32<T, V>(out + head + c, r);
+                } else {
+                    const int i0 = j * V;
+                    if (i0 < a.R) {
+                        const int ca = head + (INTER ? 2 * i0 : i0);
+                        const int cb = head + (INTER ? 2 * i0 + 1 : i0 + a.R);
+                        float fa[V], fb[V], xa[V], xb[V], ra[V], rb[V];
+                        ld_f32<T, V>(src + ca, fa);
+                        ld_f32<T, V>(src + cb, fb);
+                        if (want_pos) {
+                            ld_f32<T, V>(x + ca, xa);
+                            ld_f32<T, V>(x + cb, xb);
+                        }
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            const float2 cs = turns[i0 + e];
+                            const float s = GRAD ? -cs.y : cs.y;
+                            ra[e] = fa[e] * cs.x - fb[e] * s;
+                            rb[e] = fa[e] * s + fb[e] * cs.x;
+                            if (want_pos) {
+                                const float oa = xa[e] * cs.x - xb[e] * cs.y;
+                                const float ob = xa[e] * cs.y + xb[e] * cs.x;
+                                const float d = a.freqs[i0 + e] * (fb[e] * oa - fa[e] * ob);
+                                int ax = 0;
+                                while (ax + 1 < a.A && i0 + e >= a.pair_end[ax]) ++ax;
+#pragma unroll
+                                for (int k = 0; k < kRopeMaxAxes; ++k) acc[k] += k == ax ? d : 0.f;
+                            }
+                        }
+                        st_f32<T, V>(out + ca, ra);
+                        st_f32<T, V>(out + cb, rb);
+                    } else {
+                        const int c = head + i0 + a.R;      // 2R + (i0 - R)
+                        float f[V];
+                        ld_f32<T, V>(src + c, f);
+                        st_f32<T, V>(out + c, f);
+                    }
+                }
+            }
+        }
+    }
+    if (want_pos) {       // uniform over the grid: every lane of the warp takes part
+#pragma unroll
+        for (int k = 0; k < kRopeMaxAxes; ++k)
+            for (int o = tpt >> 1; o > 0; o >>= 1)
+                acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+        // the inverse turn's angle is -pos * freqs: a.sign is its derivative's sign
+        if (live && lane < a.A) {
+            float v = acc[0];
+#pragma unroll
+            for (int k = 1; k < kRopeMaxAxes; ++k) v = lane == k ? acc[k] : v;
+            a.grad_pos[prow * a.A + lane] = v * a.sign;
+        }
+    }
+}
+
+}  // namespace dcnb

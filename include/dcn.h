@@ -1,7 +1,9 @@
 /*
  * dcn.h - C interface of libdcn_b200.so: deformable sampling-aggregation
  * (DCNv3 / DCNv4 core) and multi-scale deformable attention (MSDeformAttn core)
- * forward and backward on NVIDIA B200 (sm_100a).
+ * forward and backward on NVIDIA B200 (sm_100a), and the operators of the
+ * attention block around them: rotary positions over several axes, differential
+ * attention, and the normed residual join of two blocks.
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The library
@@ -496,6 +498,167 @@ DCN_API int dynconv_forward(const void* x, const void* weights, void* out, int N
 DCN_API int dynconv_forward_algo(const void* x, const void* weights, void* out, int N, int H,
                  int W, int C, int G, int K, int softmax_flag, int dtype, int algo,
                  void* stream);
+
+/*
+ * axial_rope_forward - rotary positions over one to four axes.
+ *
+ * For token l of image n, every head m and pair i < R = sum(axis_pairs) of its
+ * channels: th = pos[n][l][axis(i)] * freqs[i] and
+ *   (a, b) -> (a cos th - b sin th, a sin th + b cos th),
+ * with (a, b) channels (2i, 2i + 1) (interleaved = 1) or (i, i + R)
+ * (interleaved = 0).  Axis 0 owns the first axis_pairs[0] pairs, axis 1 the
+ * next ones, and so on; channels from 2R on pass through.  inverse = 1 turns
+ * by -th.  The angle is formed in float64 and reduced to one turn there, so
+ * positions of any size keep their float32 digits.
+ *
+ * Layouts:
+ *   x      [N][L][M][D]   image stride x_image and token stride x_row (in
+ *                         elements; dense: L*M*D and M*D), [M][D] dense
+ *   pos    [pos_images][L][A]  float32; pos_images is N, or 1 (shared)
+ *   freqs  [R]            float32, radians per unit of position
+ *   out    [N][L][M][D]   dense; may be x itself when x is dense (in place)
+ *   axis_pairs            HOST array of A ints (read during the call)
+ *
+ * Limits: A <= 4, R <= 256, M * D <= 2^24, N * L < 2^31 - 1
+ * (DCN_ERR_UNSUPPORTED).  N = 0 or L = 0 launches nothing.
+ * Errors: DCN_ERR_INVALID_ARG for a bad dimension, 2R > D, pos_images neither
+ * 1 nor N, a flag not 0/1, a token stride below M*D, a negative image stride,
+ * an unknown dtype, a null pointer or an overlapping output;
+ * DCN_ERR_MISALIGNED when a pointer is not aligned to its element size.
+ */
+DCN_API int axial_rope_forward(const void* x, const float* pos, const float* freqs, void* out,
+                       const int* axis_pairs, int N, int L, int M, int D, int A, int pos_images,
+                       long long x_image, long long x_row, int interleaved, int inverse, int dtype,
+                       void* stream);
+
+/*
+ * axial_rope_backward - gradients of axial_rope_forward with respect to x and
+ * pos (grad_pos may be NULL; x is then not read and may be NULL):
+ *   grad_x   [N][L][M][D]  grad_out turned by the opposite angle
+ *   grad_pos [pos_images][L][A] float32: the sum over heads (and over the images
+ *            of a shared pos) and the axis's pairs of freqs[i] (g_b a' - g_a b'),
+ *            (a', b') the turned pair, in float32 in a fixed order
+ * grad_out is dense; the other arguments, limits and errors are those of
+ * axial_rope_forward (no in-place form).
+ */
+DCN_API int axial_rope_backward(const void* x, const float* pos, const float* freqs,
+                       const void* grad_out, void* grad_x, float* grad_pos,
+                       const int* axis_pairs, int N, int L, int M, int D, int A, int pos_images,
+                       long long x_image, long long x_row, int interleaved, int inverse, int dtype,
+                       void* stream);
+
+/*
+ * norm_residual_forward - the join of two blocks of a residual network:
+ *   u = norm(y) * post_weight + post_bias     (DCN_NORM_POST; else u = y)
+ *   z = x + scale[c] * gate[n][c] * u
+ *   h = norm(z) * pre_weight + pre_bias       (DCN_NORM_PRE; else no h)
+ * norm is the layer norm over the C channels of a row, (t - mean) / sqrt(var +
+ * eps), or with DCN_NORM_RMS t / sqrt(mean(t^2) + eps).  h is the norm of z
+ * before z is rounded.  The vectors may be NULL: weights, scale and gate are
+ * then 1, biases 0.
+ *
+ * Layouts: x, y, z, h [N][L][C]; gate [N][C]; scale, weights, biases [C]; all
+ * dense and of one dtype.  z may be x itself (in place).
+ *
+ * Limits: C <= 8192, N * L < 2^31 (DCN_ERR_UNSUPPORTED).  N = 0 or L = 0
+ * launches nothing.  Errors: DCN_ERR_INVALID_ARG for a bad dimension, unknown
+ * flags or dtype, eps < 0 or NaN, a weight or bias of a norm that is off, a null
+ * pointer or an overlapping output; DCN_ERR_MISALIGNED as elsewhere.
+ */
+enum { DCN_NORM_RMS = 1, DCN_NORM_POST = 2, DCN_NORM_PRE = 4 };
+
+DCN_API int norm_residual_forward(const void* x, const void* y, const void* scale,
+                          const void* gate, const void* post_weight, const void* post_bias,
+                          const void* pre_weight, const void* pre_bias, void* z, void* h, int N,
+                          long long L, int C, int flags, float eps, int dtype, void* stream);
+
+/* Bytes of workspace norm_residual_backward needs (gated: 1 with a gate), on the
+ * current device; DCN_ERR_INVALID_ARG or DCN_ERR_UNSUPPORTED for bad sizes. */
+DCN_API long long norm_residual_backward_workspace_size(int N, long long L, int C, int gated,
+                                                int dtype);
+
+/*
+ * norm_residual_backward - gradients of norm_residual_forward, from y, its
+ * output z (as stored), grad_z and grad_h:
+ *   grad_x, grad_y [N][L][C]; grad_gate [N][C]; the others [C]
+ * Every gradient of a factor may be NULL (not computed); grad_gate needs a
+ * gate.  Without DCN_NORM_PRE z and grad_h are not read.  The factors' sums run
+ * over float32 partial sums in `workspace` (16-byte aligned,
+ * norm_residual_backward_workspace_size bytes) in a fixed order: equal calls on
+ * one device give equal bits.  An empty batch gives zero gradients of the factors.
+ */
+DCN_API int norm_residual_backward(const void* y, const void* z, const void* grad_z,
+                           const void* grad_h, const void* scale, const void* gate,
+                           const void* post_weight, const void* post_bias,
+                           const void* pre_weight, void* grad_x, void* grad_y, void* grad_scale,
+                           void* grad_gate, void* grad_post_weight, void* grad_post_bias,
+                           void* grad_pre_weight, void* grad_pre_bias, void* workspace,
+                           long long workspace_bytes, int N, long long L, int C, int flags,
+                           float eps, int dtype, void* stream);
+
+/*
+ * diff_attn_forward - differential attention, the difference of two softmax
+ * maps with a learned weight per head.  For token i of image n, head h and its
+ * key / value head a = h / (M / Mk):
+ *   P_s[i][j] = softmax over the visible keys j of scale * <q[n][i][h][s], k[n][j][a][s]>
+ *   out[n][i][h] = sum_j (P_0[i][j] - lambda[h] P_1[i][j]) v[n][j][a],   s = 0, 1
+ * Key j of image n is visible to token i when j < lengths[n] (clamped to 0 ..
+ * Lk), mask[n][j] is 0 and, with causal = 1, j <= i + lengths[n] - Lq: the
+ * tokens are the last Lq of the image's sequence.  A token that sees no key
+ * gives zeros.  What a key that no token of the image may see (past the length
+ * or masked) holds, NaN included, does not reach any result.
+ *
+ * Layouts (channels dense, image and token strides in elements):
+ *   q [N][Lq][M][2][D], k [N][Lk][Mk][2][D], v [N][Lk][Mk][Dv]
+ *   lambda [M]; mask [N][Lk] bytes or NULL; lengths [N] int32 or NULL (Lk)
+ *   out [N][Lq][M][Dv], dense
+ * For the backward pass the call also stores (both or neither, else NULL)
+ *   out2 [N][Lq][M][Dv] dense, the second map's own output sum_j P_1 v
+ *   lse  [N][M][2][Lq] float32, log2 of the sum of exponentials of each map's
+ *        scores, +inf for a token that sees no key
+ * Scores, softmax statistics and sums are float32; with 16-bit data on the
+ * tensor cores the weights P enter the product with v rounded to that type.
+ *
+ * Limits: D <= 128, Dv <= 256, M <= 65535, N * Mk <= 65535, Lq * M / Mk and
+ * Lq + Lk below 2^31 - 65536 (DCN_ERR_UNSUPPORTED).  N = 0 or Lq = 0 launches
+ * nothing.  `workspace`: diff_attn_forward_workspace_size bytes, 16-byte
+ * aligned (NULL when that is 0).  Errors: DCN_ERR_INVALID_ARG for a bad
+ * dimension, M % Mk != 0, causal not 0/1, a scale that is not finite, a token
+ * stride below the token's size, a negative image stride, an unknown dtype, a
+ * null pointer, a small workspace or an overlapping output; DCN_ERR_MISALIGNED.
+ */
+DCN_API int diff_attn_forward(const void* q, const void* k, const void* v, const void* lambda,
+                      const unsigned char* mask, const int* lengths, void* out, void* out2,
+                      float* lse, void* workspace, long long workspace_bytes, int N, int Lq,
+                      int Lk, int M, int Mk, int D, int Dv, long long q_image, long long q_row,
+                      long long k_image, long long k_row, long long v_image, long long v_row,
+                      float scale, int causal, int dtype, void* stream);
+
+/* Bytes of workspace diff_attn_forward needs on the current device (0 when the
+ * keys are not split); DCN_ERR_INVALID_ARG or DCN_ERR_UNSUPPORTED for bad sizes. */
+DCN_API long long diff_attn_forward_workspace_size(int N, int Lq, int Lk, int M, int Mk, int D,
+                                           int Dv, int dtype);
+
+/* Bytes of workspace diff_attn_backward needs. */
+DCN_API long long diff_attn_backward_workspace_size(int N, int Lq, int M, int dtype);
+
+/*
+ * diff_attn_backward - gradients of diff_attn_forward with respect to q, k, v
+ * and lambda, from its inputs, its outputs out, out2 and lse, and grad_out
+ * (dense, as out).  The gradients are dense: grad_q [N][Lq][M][2][D], grad_k
+ * [N][Lk][Mk][2][D], grad_v [N][Lk][Mk][Dv], grad_lambda [M]; those of a key /
+ * value head are summed over its M / Mk heads.  Keys that no token sees get
+ * zeros.  No sum goes through atomics: equal calls give equal bits.
+ * Arguments, limits and errors otherwise as diff_attn_forward.
+ */
+DCN_API int diff_attn_backward(const void* q, const void* k, const void* v, const void* lambda,
+                       const unsigned char* mask, const int* lengths, const void* out,
+                       const void* out2, const float* lse, const void* grad_out, void* grad_q,
+                       void* grad_k, void* grad_v, void* grad_lambda, void* workspace,
+                       long long workspace_bytes, int N, int Lq, int Lk, int M, int Mk, int D,
+                       int Dv, long long q_image, long long q_row, long long k_image,
+                       long long k_row, long long v_image, long long v_row, float scale,
+                       int causal, int dtype, void* stream);
 
 /* Output size of the deformable window: (in + 2 pad - dil (k - 1) - 1) / stride + 1,
  * or a value <= 0 when the window does not fit. */
