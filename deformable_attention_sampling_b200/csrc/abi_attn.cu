@@ -2,6 +2,7 @@
 // their workspace sizes.
 #include "abi_common.cuh"
 #include "diff_attn.cuh"
+#include "diff_attn_mma.cuh"
 
 using namespace dcnb_abi;
 
@@ -112,9 +113,8 @@ int attn_setup(dcnb::AttnArgs* a, const void* q, const void* k, const void* v, c
         Dv <= 0 || (causal != 0 && causal != 1) || !std::isfinite(scale) || q_image < 0 ||
         k_image < 0 || v_image < 0)
         return DCN_ERR_INVALID_ARG;
-    if (D > dcnb::kAttnMaxD || Dv > dcnb::kAttnMaxDv || M > 65535 ||
-        (long long)N * Mk > 65535 || (long long)Lq * (M / Mk) > kInt31 - 65536 ||
-        (long long)Lk > kInt31 - 65536 || (long long)Lq + Lk > kInt31 - 65536)
+    if (D > dcnb::kAttnMaxD || Dv > dcnb::kAttnMaxDv || (long long)N * M > 65535 ||
+        (long long)Lq * (M / Mk) > kInt31 - 65536 || (long long)Lk > kInt31 - 65536 || (long long)Lq + Lk > kInt31 - 65536)
         return DCN_ERR_UNSUPPORTED;
     if (q_row < (long long)M * 2 * D || k_row < (long long)Mk * 2 * D ||
         v_row < (long long)Mk * Dv)
@@ -195,15 +195,15 @@ bool any_clash(const Span* outs, int n_out, const Span* ins, int n_in) {
     return false;
 }
 
-// A grid whose x counts row or key tiles and y the (image, key / value head)
-// pairs, z the splits.
-int launch_attn(const void* fn, const dcnb::AttnArgs& a, dim3 grid, int threads, int smem,
-                void* stream) {
+// A grid whose x counts row or key tiles, y the (image, head) pairs and z the
+// splits.
+template <typename Args>
+int launch_attn(const void* fn, const Args& a, dim3 grid, int threads, int smem, void* stream) {
     if (wave_size(fn, threads, smem) <= 0) {
         g_last_cuda_error = (int)cudaGetLastError();
         return DCN_ERR_CUDA;
     }
-    void* params[] = {const_cast<dcnb::AttnArgs*>(&a)};
+    void* params[] = {const_cast<Args*>(&a)};
     const cudaError_t err =
         cudaLaunchKernel(fn, grid, dim3(threads), params, (size_t)smem, (cudaStream_t)stream);
     if (err != cudaSuccess) {
@@ -213,6 +213,74 @@ int launch_attn(const void* fn, const dcnb::AttnArgs& a, dim3 grid, int threads,
     }
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return DCN_OK;
+}
+
+// The tensor-core kernels take 16-bit data whose rows are 16-byte vectors at
+// 16-byte aligned places (what tensor maps can address).
+bool mma_sizes(int dtype, int D, int Dv) {
+    return dtype != DCN_F32 && D % 8 == 0 && Dv % 8 == 0;
+}
+
+bool mma_layout(const dcnb::AttnArgs& a) {
+    const uintptr_t bits = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v;
+    const long long strides = a.q_image | a.q_row | a.k_image | a.k_row | a.v_image | a.v_row;
+    const long long limit = 1LL << 38;       // elements: a tensor map's strides end at 2^40 bytes
+    // one image has no use for its stride; 0 (a broadcast image) is no tensor-map stride
+    return bits % 16 == 0 && strides % 8 == 0 && a.Lk > 0 && a.q_row < limit && a.k_row < limit &&
+           a.v_row < limit && a.q_image < limit && a.k_image < limit && a.v_image < limit &&
+           (a.N == 1 || (a.q_image > 0 && a.k_image > 0 && a.v_image > 0));
+}
+
+// Tensor map of [N][L][heads][inner] rows, box 64 elements x 1 head x rows tokens.
+bool head_map(CUtensorMap* map, const void* p, int dtype, int inner, int heads, int L, int N,
+              long long row, long long image, int rows) {
+    const uint64_t dims[4] = {(uint64_t)inner, (uint64_t)heads, (uint64_t)L, (uint64_t)N};
+    const uint64_t strides[3] = {(uint64_t)inner * 2, (uint64_t)row * 2,
+                                 (uint64_t)(N == 1 ? row * L : image) * 2};
+    const uint32_t box[4] = {64, 1, (uint32_t)rows, 1};
+    return encode_tmap_4d(map, p, dtype == DCN_BF16, dims, strides, box);
+}
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Key splits of the tensor-core forward: one CTA a multiprocessor runs, so the
+// keys are split when the tiles leave half of them idle or more, at least two
+// key tiles each.
+int mma_splits(int N, int Lq, int Lk, int M, int Dv) {
+    const long long ctas = (long long)ceil_div(Lq, dcnb::kAmRows) * N * M *
+                           ceil_div(Dv, dcnb::kAmMaxDv);
+    long long s = sm_count() / std::max(ctas, 1LL);
+    s = std::min(s, (long long)ceil_div(Lk, dcnb::kAmKeys) / 2);
+    return (int)std::max(1LL, std::min(s, (long long)dcnb::kAttnMaxSplits));
+}
+
+// Tokens from which the 128-row tiles of the tensor-core forward are taken.
+constexpr int kMmaMinTokens = 17;
+
+int mma_forward(const dcnb::AttnArgs& a, int dtype, void* stream) {
+    dcnb::AttnMmaArgs f;
+    f.a = a;
+    f.negate = a.scale < 0.f ? 1 : 0;
+    // the kernel takes a positive scale (a negative one turns the product's sign);
+    // 0 becomes one that leaves every score 0 to float32 and -inf hidden
+    f.a.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-30f);
+    f.dchunks = ceil_div(a.D, 64);
+    f.dsteps = ceil_div(a.D, 16);
+    f.dv_parts = ceil_div(a.Dv, dcnb::kAmMaxDv);
+    const int vchunks = ceil_div(std::min(a.Dv, dcnb::kAmMaxDv), 64);
+    f.stages = 3;
+    while (f.stages > 1 && dcnb::attn_mma_smem(f.dchunks, vchunks, f.stages) > 227 * 1024)
+        --f.stages;
+    f.flags = device_flags_word();
+    if (!head_map(&f.tq, a.q, dtype, a.D, 2 * a.M, a.Lq, a.N, a.q_row, a.q_image, dcnb::kAmRows) ||
+        !head_map(&f.tk, a.k, dtype, a.D, 2 * a.Mk, a.Lk, a.N, a.k_row, a.k_image,
+                  dcnb::kAmKeys) ||
+        !head_map(&f.tv, a.v, dtype, a.Dv, a.Mk, a.Lk, a.N, a.v_row, a.v_image, dcnb::kAmKeys))
+        return DCN_ERR_UNSUPPORTED;
+    const void* fn = dtype == DCN_BF16 ? (const void*)dcnb::diff_attn_mma_kernel<__nv_bfloat16>
+                                       : (const void*)dcnb::diff_attn_mma_kernel<__half>;
+    return launch_attn(fn, f, dim3(ceil_div(a.Lq, dcnb::kAmRows), a.N * a.M, a.splits * f.dv_parts),
+                       dcnb::kAmThreads, dcnb::attn_mma_smem(f.dchunks, vchunks, f.stages), stream);
 }
 
 template <typename T>
@@ -230,9 +298,12 @@ long long diff_attn_forward_workspace_size(int N, int Lq, int Lk, int M, int Mk,
                               M, Mk, D, Dv, 0, qd, 0, kd, 0, vd, 1.f, 0, dtype);
     if (st != DCN_OK) return st;
     if (N == 0 || Lq == 0) return 0;
-    const AttnPlan p = attn_plan(N, Lq, Lk, M, Mk);
-    if (p.splits == 1) return 0;
-    return (long long)p.splits * N * M * Lq * 2 * (2 + (long long)Dv) * 4;
+    // which kernel runs depends on the addresses too: enough for either
+    int splits = attn_plan(N, Lq, Lk, M, Mk).splits;
+    if (mma_sizes(dtype, D, Dv) && Lq >= kMmaMinTokens)
+        splits = std::max(splits, mma_splits(N, Lq, Lk, M, Dv));
+    if (splits == 1) return 0;
+    return (long long)splits * N * M * Lq * 2 * (2 + (long long)Dv) * 4;
 }
 
 int diff_attn_forward(const void* q, const void* k, const void* v, const void* lambda,
@@ -253,6 +324,8 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
         (uintptr_t)workspace % 16 != 0)
         return DCN_ERR_MISALIGNED;
     const AttnPlan p = attn_plan(N, Lq, Lk, M, Mk);
+    const bool mma = mma_sizes(dtype, D, Dv) && Lq >= kMmaMinTokens && mma_layout(a) &&
+                     ((uintptr_t)out | (uintptr_t)out2) % 16 == 0;
     const long long need = diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return DCN_ERR_INVALID_ARG;
     const long long ob = (long long)N * Lq * M * Dv * es;
@@ -264,11 +337,11 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
     a.out = out;
     a.out2 = out2;
     a.lse = lse;
-    a.splits = p.splits;
+    a.splits = mma ? mma_splits(N, Lq, Lk, M, Dv) : p.splits;
     const long long rows_total = (long long)N * M * Lq;
-    if (p.splits > 1) {
+    if (a.splits > 1) {
         a.part_o = static_cast<float*>(workspace);
-        a.part_ml = a.part_o + (long long)p.splits * rows_total * 2 * Dv;
+        a.part_ml = a.part_o + (long long)a.splits * rows_total * 2 * Dv;
     }
     const int ct = columns(Dv);
     const void* fn = nullptr;
@@ -283,9 +356,10 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
         default: break;
     }
     if (!fn) return DCN_ERR_UNSUPPORTED;
-    rc = launch_attn(fn, a, dim3(p.tiles, N * Mk, p.splits), dcnb::kAttnThreads,
-                     dcnb::attn_fwd_smem(p.bq, D, ct), stream);
-    if (rc != DCN_OK || p.splits == 1) return rc;
+    rc = mma ? mma_forward(a, dtype, stream)
+             : launch_attn(fn, a, dim3(p.tiles, N * Mk, a.splits), dcnb::kAttnThreads,
+                           dcnb::attn_fwd_smem(p.bq, D, ct), stream);
+    if (rc != DCN_OK || a.splits == 1) return rc;
     return launch_attn(join, a, dim3((unsigned)((rows_total + 7) / 8)), 256, 0, stream);
 }
 

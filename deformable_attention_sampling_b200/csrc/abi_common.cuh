@@ -149,4 +149,11 @@ unsigned int* device_flags_word();
 bool encode_tmap_2d(CUtensorMap* map, const void* base, bool bf16, uint64_t inner,
                     uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
 
+// A 4-D tensor map over 16-bit elements with dimensions dims[0] (dense) ..
+// dims[3], the last three `strides` bytes apart, for tile loads of box[0] = 64
+// elements x box[1] x box[2] x box[3] with the 128-byte swizzle; out-of-range
+// elements read as zero.  False on any error.
+bool encode_tmap_4d(CUtensorMap* map, const void* base, bool bf16, const uint64_t dims[4],
+                    const uint64_t strides[3], const uint32_t box[4]);
+
 }  // namespace dcnb_abi

@@ -1,0 +1,414 @@
+// Differential attention on the tensor cores (tcgen05, accumulators in TMEM),
+// forward, 16-bit types (sm_100a).  The mathematics is diff_attn.cuh's.
+//
+// One CTA owns 128 tokens of one head and walks the keys in tiles of 128, with
+// both softmax maps in flight: while the softmax warps of map 0 work on their
+// tile, the tensor cores run the products of map 1, and the other way round.
+//   producer (one thread)   tensor-map loads of the tokens' two query tiles,
+//             then per tile the two key tiles and the value tile (128-byte
+//             swizzle, rows past the tensor read as zeros);
+//   MMA       (one thread)  S_m = Q_m K_m^T (float32, 128 TMEM columns a map)
+//             and O_m += P_m V, P_m as the left operand from TMEM, V from the
+//             shared tile as it lies (N-major);
+//   softmax   (four warps a map, thread = token) reads its row of S_m, keeps
+//             the running maximum and sum, writes P_m in 16 bits over S_m.
+// TMEM: S_0, S_1 128 columns each, O_0, O_1 up to 128 columns each: all 512.
+//
+// The running maximum is lowered into O only when it has grown by more than
+// 2^8 (the weights stay below 2^8 then, or 2^14 with fp16's bias): O_m lives in
+// TMEM, and a rescale is a round trip through registers that nearly no tile
+// needs.  fp16 weights carry a factor 2^6, so that weights down to 2^-20 of
+// the largest stay normal numbers.  Weights enter the product rounded to the
+// type (half a step of the type each), their sum is that of the unrounded ones.
+//
+// Keys that no token may see (past the length, masked) get weight 0, and the
+// MMA warp zeroes their value rows in the tile first: 0 times what lies there
+// must not be NaN.
+//
+// Bound: per 128 x 128 tile and map the exponentials take 1024 cycles of the
+// special-function units and the products 768 (D = 64, Dv = 128).
+#pragma once
+
+#include "diff_attn.cuh"
+#include "tmem.cuh"
+
+namespace dcnb {
+
+constexpr int kAmRows = 128;                 // tokens of a CTA
+constexpr int kAmKeys = 128;                 // keys of a tile
+constexpr int kAmThreads = 384;              // 2 x 4 softmax warps, producer, MMA, 2 idle
+constexpr int kAmChunkBytes = 128 * 128;     // 128 rows of 64 16-bit elements
+constexpr int kAmMaxDv = 128;                // value columns of a CTA
+constexpr float kAmLazy = 8.f;
+
+struct AttnMmaArgs {
+    CUtensorMap tq;            // [N][Lq][2 M][D], box {64, 1, 128, 1}
+    CUtensorMap tk;            // [N][Lk][2 Mk][D]
+    CUtensorMap tv;            // [N][Lk][Mk][Dv]
+    AttnArgs a;
+    unsigned int* flags;
+    int dchunks;               // 64-column chunks of a head
+    int dsteps;                // K = 16 steps of a head
+    int dv_parts;              // CTAs that share a head's value columns
+    int stages;
+    int negate;                // the scale is negative
+};
+
+// Bits of the 32 keys from j on that some token may see.
+__device__ __forceinline__ uint32_t attn_key_bits(const AttnArgs& a, int n, int j, int len,
+                                                  int lane) {
+    const int key = j + lane;
+    const bool ok = key < len && !(a.mask && a.mask[(long long)n * a.Lk + key]);
+    return __ballot_sync(0xffffffffu, ok);
+}
+
+__host__ __device__ constexpr int attn_mma_smem(int dchunks, int vchunks, int stages) {
+    return 1024 + (2 * dchunks + stages * (2 * dchunks + vchunks)) * kAmChunkBytes + 4096;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAmThreads, 1)
+    diff_attn_mma_kernel(const __grid_constant__ AttnMmaArgs f) {
+    constexpr float kBias = std::is_same<T, __half>::value ? 6.f : 0.f;
+    const AttnArgs& a = f.a;
+    const int NS = f.stages, DCH = f.dchunks;
+    extern __shared__ __align__(128) unsigned char am_smem[];
+    unsigned char* base = am_smem + ((1024u - (smem_u32(am_smem) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const int part = (int)blockIdx.z % f.dv_parts, split = (int)blockIdx.z / f.dv_parts;
+    const int c0 = part * kAmMaxDv;
+    const int dv = min(a.Dv - c0, kAmMaxDv);         // value columns of this CTA
+    const int dvn = (dv + 15) & ~15;                 // N of the value product
+    const int vch = (dv + 63) >> 6;
+    const int n = (int)blockIdx.y / a.M, head = (int)blockIdx.y - n * a.M, kv = head / a.G;
+    // in causal order the last tiles see the most keys: they start first
+    const int q0 = (int)(gridDim.x - 1 - blockIdx.x) * kAmRows;
+    const int len = attn_len(a, n);
+    const int last = min(q0 + kAmRows, a.Lq) - 1;
+    const int kmax = a.causal ? max(0, min(len, last + len - a.Lq + 1)) : len;
+    const int tiles = (kmax + kAmKeys - 1) / kAmKeys;
+    const int t0 = (int)((long long)tiles * split / a.splits);
+    const int t1 = (int)((long long)tiles * (split + 1) / a.splits);
+    const int count = t1 - t0;
+
+    unsigned char* qs = base;                                   // [2][DCH] chunks
+    unsigned char* ks = qs + 2 * DCH * kAmChunkBytes;           // [NS][2][DCH]
+    unsigned char* vs = ks + NS * 2 * DCH * kAmChunkBytes;      // [NS][vch of the launch]
+    const int vstage = ((min(a.Dv, kAmMaxDv) + 63) >> 6) * kAmChunkBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(vs + NS * vstage);
+    uint64_t* q_full = bars;
+    uint64_t* k_full = q_full + 1;
+    uint64_t* k_empty = k_full + NS;
+    uint64_t* v_full = k_empty + NS;
+    uint64_t* v_empty = v_full + NS;
+    uint64_t* s_full = v_empty + NS;      // [2] scores of a map written
+    uint64_t* p_full = s_full + 2;        // [2] weights of a map written
+    uint64_t* o_done = p_full + 2;        // [2] value product of a map done
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+    uint32_t* vis = tmem_slot + 4;                                // [NS][4] key bits of a tile
+    float* inv = reinterpret_cast<float*>(vis + NS * 4);          // [2][128]
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        for (int m = 0; m < 2; ++m) {
+            mbar_init(&s_full[m], 1);
+            mbar_init(&p_full[m], 4);
+            mbar_init(&o_done[m], 1);
+        }
+        mbar_fence_init();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_u32(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // registers: 384 threads at 168; the softmax warps take 216 (2 x 128 x 216 + 128 x 72 =
+    // 384 x 168), enough for a row of 128 scores
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    }
+    if (warp == 8) {
+        // ------------------------------------------------------------ producer
+        bool ok = true;
+        int loaded = 0;
+        if (count > 0 && lane == 0) {
+            mbar_arrive_expect_tx(q_full, (uint32_t)(2 * DCH * kAmChunkBytes));
+            for (int m = 0; m < 2; ++m)
+                for (int c = 0; c < DCH; ++c)
+                    tma_load_4d(qs + (m * DCH + c) * kAmChunkBytes, &f.tq, c * 64, head * 2 + m, q0,
+                                n, q_full);
+        }
+        for (int i = 0; i < count && ok; ++i) {
+            const int st = i % NS, j0 = (t0 + i) * kAmKeys;
+            const uint32_t ph = (uint32_t)((i / NS - 1) & 1);
+            if (i >= NS) ok = mbar_wait(&k_empty[st], ph, f.flags);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&k_full[st], (uint32_t)(2 * DCH * kAmChunkBytes));
+                for (int m = 0; m < 2; ++m)
+                    for (int c = 0; c < DCH; ++c)
+                        tma_load_4d(ks + ((st * 2 + m) * DCH + c) * kAmChunkBytes, &f.tk, c * 64,
+                                    kv * 2 + m, j0, n, &k_full[st]);
+            }
+            if (i >= NS) ok = mbar_wait(&v_empty[st], ph, f.flags);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t bits = attn_key_bits(a, n, j0 + 32 * w, len, lane);
+                if (lane == 0) vis[st * 4 + w] = bits;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&v_full[st], (uint32_t)(vch * kAmChunkBytes));
+                for (int c = 0; c < vch; ++c)
+                    tma_load_4d(vs + st * vstage + c * kAmChunkBytes, &f.tv, c0 + c * 64, kv, j0, n,
+                                &v_full[st]);
+            }
+            __syncwarp();
+            loaded = i + 1;
+        }
+        // leave only once the copies in flight have landed
+        if (count > 0) (void)mbar_wait(q_full, 0, f.flags);
+        for (int i = max(0, loaded - NS); i < loaded; ++i) {
+            (void)mbar_wait(&k_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
+            (void)mbar_wait(&v_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
+        }
+    } else if (warp == 9) {
+        // ----------------------------------------------------------------- MMA
+        const uint32_t id_s = umma_idesc<T>(kAmKeys, false, f.negate != 0);
+        const uint32_t id_o = umma_idesc<T>(dvn, true, false);
+        const uint32_t q_s = smem_u32(qs), k_s = smem_u32(ks), v_s = smem_u32(vs);
+        auto scores = [&](int i, int m) {
+            const uint32_t qa = q_s + m * DCH * kAmChunkBytes;
+            const uint32_t kb = k_s + ((i % NS) * 2 + m) * DCH * kAmChunkBytes;
+            for (int k = 0; k < f.dsteps; ++k) {
+                const uint32_t off = (uint32_t)(k >> 2) * kAmChunkBytes + 32 * (k & 3);
+                umma_f16(tmem + m * 128, umma_desc128(qa + off, 16), umma_desc128(kb + off, 16),
+                         id_s, k != 0 ? 1u : 0u);
+            }
+            umma_commit(&s_full[m]);
+        };
+        bool ok = count > 0 && mbar_wait(q_full, 0, f.flags) && mbar_wait(&k_full[0], 0, f.flags);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && lane == 0) {
+            tmem_fence_after();
+            scores(0, 0);
+            scores(0, 1);
+            umma_commit(&k_empty[0]);
+        }
+        for (int i = 0; i < count && ok; ++i) {
+            const int st = i % NS;
+            ok = mbar_wait(&v_full[st], (uint32_t)((i / NS) & 1), f.flags);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            for (int w = 0; w < 4; ++w) {
+                uint32_t hidden = ~vis[st * 4 + w];
+                if (hidden == 0) continue;
+                // 8 lanes a row of a chunk, 4 rows at a time
+                for (int r = lane >> 3; r < 32; r += 4)
+                    if (hidden >> r & 1)
+                        for (int c = 0; c < vch; ++c)
+                            *reinterpret_cast<uint4*>(vs + st * vstage + c * kAmChunkBytes +
+                                                      (w * 32 + r) * 128 + (lane & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+            }
+            fence_async_shared();
+            __syncwarp();
+            for (int m = 0; m < 2 && ok; ++m) {
+                ok = mbar_wait(&p_full[m], (uint32_t)(i & 1), f.flags);
+                if (m == 0 && i + 1 < count)
+                    ok = ok && mbar_wait(&k_full[(i + 1) % NS],
+                                         (uint32_t)(((i + 1) / NS) & 1), f.flags);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    tmem_fence_after();
+                    for (int k = 0; k < kAmKeys / 16; ++k)
+                        umma_f16_ta(tmem + 256 + m * 128, tmem + m * 128 + k * 8,
+                                    umma_desc128(v_s + st * vstage + k * 2048, kAmChunkBytes), id_o,
+                                    (i | k) != 0 ? 1u : 0u);
+                    umma_commit(&o_done[m]);
+                    if (m == 1) umma_commit(&v_empty[st]);
+                    if (i + 1 < count) {
+                        scores(i + 1, m);
+                        if (m == 1) umma_commit(&k_empty[(i + 1) % NS]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------------------- softmax
+        const int m = warp >> 2, quarter = warp & 3;
+        const int row = quarter * 32 + lane, tok = q0 + row;
+        const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + m * 128;
+        const uint32_t t_o = t_s - m * 128 + 256 + m * 128;
+        const int limit = a.causal ? min(len, tok + len - a.Lq + 1) : len;
+        const float sc = a.scale_log2;
+        float top = -INFINITY, sum = 0.f;        // reference maximum of the weights, their sum
+        bool ok = true;
+        for (int i = 0; i < count; ++i) {
+            const int st = i % NS, j0 = (t0 + i) * kAmKeys;
+            ok = mbar_wait(&s_full[m], (uint32_t)(i & 1), f.flags);
+            if (ok && a.mask) ok = mbar_wait(&v_full[st], (uint32_t)((i / NS) & 1), f.flags);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            tmem_fence_after();
+            uint32_t r[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, r + 32 * c);
+            tmem_wait_ld();
+            float* s = reinterpret_cast<float*>(r);
+            const int cnt = limit - j0;
+            if (!__all_sync(0xffffffffu, cnt >= kAmKeys) || a.mask) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t bits = a.mask ? vis[st * 4 + w] : 0xffffffffu;
+                    const int in = cnt - 32 * w;
+                    bits = in >= 32 ? bits : in <= 0 ? 0u : bits & ((1u << in) - 1u);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        s[32 * w + c] = bits >> c & 1 ? s[32 * w + c] : -INFINITY;
+                }
+            }
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mx[c] = s[c];
+#pragma unroll
+            for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+            const float hi = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc - kBias;
+            const bool first = top == -INFINITY;
+            const bool grow = !first && hi > top + kAmLazy;
+            if (__any_sync(0xffffffffu, grow)) {
+                // the last value product has to be in O_m
+                ok = __all_sync(0xffffffffu, mbar_wait(&o_done[m], (uint32_t)((i - 1) & 1), f.flags));
+                if (!ok) break;
+                tmem_fence_after();
+                const float keep = grow ? ex2(top - hi) : 1.f;
+                for (int c = 0; c < dvn; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(t_o + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                    tmem_st16(t_o + c, o);
+                }
+                sum *= keep;
+                if (grow) top = hi;
+            }
+            if (first) top = hi;
+            const float ref = top == -INFINITY ? 0.f : top;
+            const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const int at = 64 * h + 2 * c;
+                    float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), sc2, rf2);
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    acc[c & 1] = __fadd2_rn(acc[c & 1], x);
+                    p[c] = Elem<T>::pack2(x.x, x.y);
+                }
+                tmem_st32(t_s + 32 * h, p);
+            }
+            sum += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[m]);
+        }
+        // ------------------------------------------------------------ epilogue
+        if (ok && count > 0) {
+            ok = mbar_wait(&o_done[0], (uint32_t)((count - 1) & 1), f.flags);
+            ok = mbar_wait(&o_done[1], (uint32_t)((count - 1) & 1), f.flags) && ok;
+        }
+        tmem_fence_after();
+        inv[m * 128 + row] = sum > 0.f ? 1.f / sum : 0.f;
+        const bool live = tok < a.Lq;
+        const bool lead = part == 0 && live;
+        const long long rows_total = (long long)a.N * a.M * a.Lq;
+        // packed row of the join kernel: token * G + head within its group
+        const long long at = (long long)split * rows_total +
+                             ((long long)n * a.Mk + kv) * a.rows + (long long)tok * a.G + head -
+                             kv * a.G;
+        if (a.splits > 1) {
+            if (lead) {
+                a.part_ml[(at * 2 + m) * 2] = top;
+                a.part_ml[(at * 2 + m) * 2 + 1] = sum;
+            }
+        } else if (a.lse && lead) {
+            a.lse[(((long long)n * a.M + head) * 2 + m) * a.Lq + tok] =
+                sum > 0.f ? top + log2f(sum) : INFINITY;
+        }
+        named_barrier(1, 256);
+        const float i0 = inv[row], i1 = inv[128 + row];
+        const float lam = Elem<T>::one(static_cast<const T*>(a.lam) + head);
+        const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16) + 256;
+        const long long to = (((long long)n * a.Lq + tok) * a.M + head) * a.Dv + c0;
+        for (int c = 16 * m; c < dvn; c += 32) {
+            uint32_t o0[16], o1[16];
+            if (count > 0) {
+                tmem_ld16(t_row + c, o0);
+                tmem_ld16(t_row + 128 + c, o1);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o0[e] = o1[e] = 0u;
+            }
+            if (live && a.splits > 1) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    if (c + e < dv) {
+                        float* d = a.part_o + at * 2 * a.Dv + c0 + c + e;
+                        *reinterpret_cast<uint4*>(d) =
+                            make_uint4(o0[e], o0[e + 1], o0[e + 2], o0[e + 3]);
+                        *reinterpret_cast<uint4*>(d + a.Dv) =
+                            make_uint4(o1[e], o1[e + 1], o1[e + 2], o1[e + 3]);
+                    }
+            } else if (live) {
+                float x[16], y[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    y[e] = __uint_as_float(o1[e]) * i1;
+                    x[e] = __uint_as_float(o0[e]) * i0 - lam * y[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e += 8)
+                    if (c + e < dv) {
+                        st_f32<T, 8>(static_cast<T*>(a.out) + to + c + e, x + e);
+                        if (a.out2) st_f32<T, 8>(static_cast<T*>(a.out2) + to + c + e, y + e);
+                    }
+            }
+            __syncwarp();
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;"
+                     :: "r"(tmem) : "memory");
+    }
+}
+
+}  // namespace dcnb

@@ -619,7 +619,7 @@ DCN_API int norm_residual_backward(const void* y, const void* z, const void* gra
  * Scores, softmax statistics and sums are float32; with 16-bit data on the
  * tensor cores the weights P enter the product with v rounded to that type.
  *
- * Limits: D <= 128, Dv <= 256, M <= 65535, N * Mk <= 65535, Lq * M / Mk and
+ * Limits: D <= 128, Dv <= 256, N * M <= 65535, Lq * M / Mk and
  * Lq + Lk below 2^31 - 65536 (DCN_ERR_UNSUPPORTED).  N = 0 or Lq = 0 launches
  * nothing.  `workspace`: diff_attn_forward_workspace_size bytes, 16-byte
  * aligned (NULL when that is 0).  Errors: DCN_ERR_INVALID_ARG for a bad
