@@ -114,7 +114,7 @@ int attn_setup(dcnb::AttnArgs* a, const void* q, const void* k, const void* v, c
         k_image < 0 || v_image < 0)
         return DCN_ERR_INVALID_ARG;
     if (D > dcnb::kAttnMaxD || Dv > dcnb::kAttnMaxDv || (long long)N * M > 65535 ||
-        (long long)Lq * (M / Mk) > kInt31 - 65536 || (long long)Lk > kInt31 - 65536 || (long long)Lq + Lk > kInt31 - 65536)
+        (long long)Lq * (M / Mk) > kInt31 - 65536 || (long long)Lq + Lk > kInt31 - 65536)
         return DCN_ERR_UNSUPPORTED;
     if (q_row < (long long)M * 2 * D || k_row < (long long)Mk * 2 * D ||
         v_row < (long long)Mk * Dv)
@@ -257,6 +257,12 @@ int mma_splits(int N, int Lq, int Lk, int M, int Dv) {
 // Tokens from which the 128-row tiles of the tensor-core forward are taken.
 constexpr int kMmaMinTokens = 17;
 
+template <typename T>
+const void* mma_kernel(int dchunks) {
+    return dchunks == 1 ? (const void*)dcnb::diff_attn_mma_kernel<T, 1>
+                        : (const void*)dcnb::diff_attn_mma_kernel<T, 2>;
+}
+
 int mma_forward(const dcnb::AttnArgs& a, int dtype, void* stream) {
     dcnb::AttnMmaArgs f;
     f.a = a;
@@ -264,12 +270,13 @@ int mma_forward(const dcnb::AttnArgs& a, int dtype, void* stream) {
     // the kernel takes a positive scale (a negative one turns the product's sign);
     // 0 becomes one that leaves every score 0 to float32 and -inf hidden
     f.a.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-30f);
-    f.dchunks = ceil_div(a.D, 64);
+    const int dchunks = ceil_div(a.D, 64);
     f.dsteps = ceil_div(a.D, 16);
     f.dv_parts = ceil_div(a.Dv, dcnb::kAmMaxDv);
     const int vchunks = ceil_div(std::min(a.Dv, dcnb::kAmMaxDv), 64);
-    f.stages = 3;
-    while (f.stages > 1 && dcnb::attn_mma_smem(f.dchunks, vchunks, f.stages) > 227 * 1024)
+    f.heads = a.N * a.M;
+    f.stages = 4;
+    while (f.stages > 2 && dcnb::attn_mma_smem(dchunks, vchunks, f.stages) > 227 * 1024)
         --f.stages;
     f.flags = device_flags_word();
     if (!head_map(&f.tq, a.q, dtype, a.D, 2 * a.M, a.Lq, a.N, a.q_row, a.q_image, dcnb::kAmRows) ||
@@ -277,10 +284,12 @@ int mma_forward(const dcnb::AttnArgs& a, int dtype, void* stream) {
                   dcnb::kAmKeys) ||
         !head_map(&f.tv, a.v, dtype, a.Dv, a.Mk, a.Lk, a.N, a.v_row, a.v_image, dcnb::kAmKeys))
         return DCN_ERR_UNSUPPORTED;
-    const void* fn = dtype == DCN_BF16 ? (const void*)dcnb::diff_attn_mma_kernel<__nv_bfloat16>
-                                       : (const void*)dcnb::diff_attn_mma_kernel<__half>;
-    return launch_attn(fn, f, dim3(ceil_div(a.Lq, dcnb::kAmRows), a.N * a.M, a.splits * f.dv_parts),
-                       dcnb::kAmThreads, dcnb::attn_mma_smem(f.dchunks, vchunks, f.stages), stream);
+    const void* fn = dtype == DCN_BF16 ? mma_kernel<__nv_bfloat16>(dchunks)
+                                       : mma_kernel<__half>(dchunks);
+    const long long blocks = (long long)ceil_div(a.Lq, dcnb::kAmRows) * f.heads;
+    if (blocks > kInt31) return DCN_ERR_UNSUPPORTED;
+    return launch_attn(fn, f, dim3((unsigned)blocks, a.splits * f.dv_parts), dcnb::kAmThreads,
+                       dcnb::attn_mma_smem(dchunks, vchunks, f.stages), stream);
 }
 
 template <typename T>

@@ -1,18 +1,20 @@
 // Differential attention on the tensor cores (tcgen05, accumulators in TMEM),
 // forward, 16-bit types (sm_100a).  The mathematics is diff_attn.cuh's.
 //
-// One CTA owns 128 tokens of one head and walks the keys in tiles of 128, with
-// both softmax maps in flight: while the softmax warps of map 0 work on their
-// tile, the tensor cores run the products of map 1, and the other way round.
+// One CTA owns 128 tokens of one head and walks the keys in tiles of 64, with
+// both softmax maps in flight and two score buffers a map: the tensor cores run
+// up to two tiles ahead, so that the softmax warps find their next scores ready.
 //   producer (one thread)   tensor-map loads of the tokens' two query tiles,
 //             then per tile the two key tiles and the value tile (128-byte
 //             swizzle, rows past the tensor read as zeros);
-//   MMA       (one thread)  S_m = Q_m K_m^T (float32, 128 TMEM columns a map)
+//   MMA       (one thread)  S_m = Q_m K_m^T (float32, 64 TMEM columns a buffer)
 //             and O_m += P_m V, P_m as the left operand from TMEM, V from the
 //             shared tile as it lies (N-major);
 //   softmax   (four warps a map, thread = token) reads its row of S_m, keeps
 //             the running maximum and sum, writes P_m in 16 bits over S_m.
-// TMEM: S_0, S_1 128 columns each, O_0, O_1 up to 128 columns each: all 512.
+// TMEM: S_0, S_1 two buffers of 64 columns each, O_0, O_1 up to 128 columns
+// each: all 512.  The products of one CTA run in the order of their issue:
+// S_m(i + 2) goes out after P_m(i) V, whose left operand it overwrites.
 //
 // The running maximum is lowered into O only when it has grown by more than
 // 2^8 (the weights stay below 2^8 then, or 2^14 with fp16's bias): O_m lives in
@@ -25,8 +27,8 @@
 // MMA warp zeroes their value rows in the tile first: 0 times what lies there
 // must not be NaN.
 //
-// Bound: per 128 x 128 tile and map the exponentials take 1024 cycles of the
-// special-function units and the products 768 (D = 64, Dv = 128).
+// Bound: per 128 x 64 tile and map the exponentials take 512 cycles of the
+// special-function units and the products 384 (D = 64, Dv = 128).
 #pragma once
 
 #include "diff_attn.cuh"
@@ -35,23 +37,37 @@
 namespace dcnb {
 
 constexpr int kAmRows = 128;                 // tokens of a CTA
-constexpr int kAmKeys = 128;                 // keys of a tile
-constexpr int kAmThreads = 384;              // 2 x 4 softmax warps, producer, MMA, 2 idle
-constexpr int kAmChunkBytes = 128 * 128;     // 128 rows of 64 16-bit elements
+constexpr int kAmKeys = 64;                  // keys of a tile
+constexpr int kAmThreads = 320;              // 2 x 4 softmax warps, producer, MMA
+constexpr int kAmQBytes = kAmRows * 128;     // 64 columns of the query tile, of a
+constexpr int kAmKBytes = kAmKeys * 128;     // key or value tile (16-bit elements)
 constexpr int kAmMaxDv = 128;                // value columns of a CTA
 constexpr float kAmLazy = 8.f;
 
 struct AttnMmaArgs {
     CUtensorMap tq;            // [N][Lq][2 M][D], box {64, 1, 128, 1}
-    CUtensorMap tk;            // [N][Lk][2 Mk][D]
-    CUtensorMap tv;            // [N][Lk][Mk][Dv]
+    CUtensorMap tk;            // [N][Lk][2 Mk][D], box {64, 1, 64, 1}
+    CUtensorMap tv;            // [N][Lk][Mk][Dv], likewise
     AttnArgs a;
     unsigned int* flags;
-    int dchunks;               // 64-column chunks of a head
     int dsteps;                // K = 16 steps of a head
     int dv_parts;              // CTAs that share a head's value columns
     int stages;
     int negate;                // the scale is negative
+    int heads;                 // N * M
+};
+
+// Position in a ring of stages and the parity of the round.
+struct Ring {
+    int n, st;
+    uint32_t phase;
+    __device__ __forceinline__ explicit Ring(int stages) : n(stages), st(0), phase(0) {}
+    __device__ __forceinline__ void next() {
+        if (++st == n) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 // Bits of the 32 keys from j on that some token may see.
@@ -63,27 +79,30 @@ __device__ __forceinline__ uint32_t attn_key_bits(const AttnArgs& a, int n, int 
 }
 
 __host__ __device__ constexpr int attn_mma_smem(int dchunks, int vchunks, int stages) {
-    return 1024 + (2 * dchunks + stages * (2 * dchunks + vchunks)) * kAmChunkBytes + 4096;
+    return 1024 + 2 * dchunks * kAmQBytes + stages * (2 * dchunks + vchunks) * kAmKBytes + 4096;
 }
 
-template <typename T>
+// DCH: 64-column chunks of a head (the 16-column steps past D are skipped).
+template <typename T, int DCH>
 __global__ void __launch_bounds__(kAmThreads, 1)
     diff_attn_mma_kernel(const __grid_constant__ AttnMmaArgs f) {
     constexpr float kBias = std::is_same<T, __half>::value ? 6.f : 0.f;
     const AttnArgs& a = f.a;
-    const int NS = f.stages, DCH = f.dchunks;
+    const int NS = f.stages;
     extern __shared__ __align__(128) unsigned char am_smem[];
     unsigned char* base = am_smem + ((1024u - (smem_u32(am_smem) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    const int part = (int)blockIdx.z % f.dv_parts, split = (int)blockIdx.z / f.dv_parts;
+    const int part = (int)blockIdx.y % f.dv_parts, split = (int)blockIdx.y / f.dv_parts;
     const int c0 = part * kAmMaxDv;
     const int dv = min(a.Dv - c0, kAmMaxDv);         // value columns of this CTA
     const int dvn = (dv + 15) & ~15;                 // N of the value product
     const int vch = (dv + 63) >> 6;
-    const int n = (int)blockIdx.y / a.M, head = (int)blockIdx.y - n * a.M, kv = head / a.G;
-    // in causal order the last tiles see the most keys: they start first
-    const int q0 = (int)(gridDim.x - 1 - blockIdx.x) * kAmRows;
+    // in causal order the last tiles see the most keys: those of all heads start first
+    const int tile = (int)(blockIdx.x / (unsigned)f.heads);
+    const int nh = (int)blockIdx.x - tile * f.heads;
+    const int n = nh / a.M, head = nh - n * a.M, kv = head / a.G;
+    const int q0 = ((int)(gridDim.x / (unsigned)f.heads) - 1 - tile) * kAmRows;
     const int len = attn_len(a, n);
     const int last = min(q0 + kAmRows, a.Lq) - 1;
     const int kmax = a.causal ? max(0, min(len, last + len - a.Lq + 1)) : len;
@@ -93,21 +112,21 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     const int count = t1 - t0;
 
     unsigned char* qs = base;                                   // [2][DCH] chunks
-    unsigned char* ks = qs + 2 * DCH * kAmChunkBytes;           // [NS][2][DCH]
-    unsigned char* vs = ks + NS * 2 * DCH * kAmChunkBytes;      // [NS][vch of the launch]
-    const int vstage = ((min(a.Dv, kAmMaxDv) + 63) >> 6) * kAmChunkBytes;
+    unsigned char* ks = qs + 2 * DCH * kAmQBytes;               // [NS][2][DCH]
+    unsigned char* vs = ks + NS * 2 * DCH * kAmKBytes;          // [NS][vch of the launch]
+    const int vstage = ((min(a.Dv, kAmMaxDv) + 63) >> 6) * kAmKBytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(vs + NS * vstage);
     uint64_t* q_full = bars;
     uint64_t* k_full = q_full + 1;
     uint64_t* k_empty = k_full + NS;
     uint64_t* v_full = k_empty + NS;
     uint64_t* v_empty = v_full + NS;
-    uint64_t* s_full = v_empty + NS;      // [2] scores of a map written
-    uint64_t* p_full = s_full + 2;        // [2] weights of a map written
-    uint64_t* o_done = p_full + 2;        // [2] value product of a map done
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
-    uint32_t* vis = tmem_slot + 4;                                // [NS][4] key bits of a tile
-    float* inv = reinterpret_cast<float*>(vis + NS * 4);          // [2][128]
+    uint64_t* s_full = v_empty + NS;      // [map][buffer] scores written
+    uint64_t* p_full = s_full + 4;        // [map][buffer] weights written
+    uint64_t* o_done = p_full + 4;        // [map][buffer] value product done
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 4);
+    uint32_t* vis = tmem_slot + 4;                                // [NS][2] key bits of a tile
+    float* inv = reinterpret_cast<float*>(vis + NS * 2);          // [2][128]
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -117,7 +136,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], 1);
         }
-        for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < 4; ++m) {
             mbar_init(&s_full[m], 1);
             mbar_init(&p_full[m], 4);
             mbar_init(&o_done[m], 1);
@@ -134,152 +153,37 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     tmem_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // registers: 384 threads at 168; the softmax warps take 216 (2 x 128 x 216 + 128 x 72 =
-    // 384 x 168), enough for a row of 128 scores
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    }
-    if (warp == 8) {
-        // ------------------------------------------------------------ producer
-        bool ok = true;
-        int loaded = 0;
-        if (count > 0 && lane == 0) {
-            mbar_arrive_expect_tx(q_full, (uint32_t)(2 * DCH * kAmChunkBytes));
-            for (int m = 0; m < 2; ++m)
-                for (int c = 0; c < DCH; ++c)
-                    tma_load_4d(qs + (m * DCH + c) * kAmChunkBytes, &f.tq, c * 64, head * 2 + m, q0,
-                                n, q_full);
-        }
-        for (int i = 0; i < count && ok; ++i) {
-            const int st = i % NS, j0 = (t0 + i) * kAmKeys;
-            const uint32_t ph = (uint32_t)((i / NS - 1) & 1);
-            if (i >= NS) ok = mbar_wait(&k_empty[st], ph, f.flags);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&k_full[st], (uint32_t)(2 * DCH * kAmChunkBytes));
-                for (int m = 0; m < 2; ++m)
-                    for (int c = 0; c < DCH; ++c)
-                        tma_load_4d(ks + ((st * 2 + m) * DCH + c) * kAmChunkBytes, &f.tk, c * 64,
-                                    kv * 2 + m, j0, n, &k_full[st]);
-            }
-            if (i >= NS) ok = mbar_wait(&v_empty[st], ph, f.flags);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t bits = attn_key_bits(a, n, j0 + 32 * w, len, lane);
-                if (lane == 0) vis[st * 4 + w] = bits;
-            }
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&v_full[st], (uint32_t)(vch * kAmChunkBytes));
-                for (int c = 0; c < vch; ++c)
-                    tma_load_4d(vs + st * vstage + c * kAmChunkBytes, &f.tv, c0 + c * 64, kv, j0, n,
-                                &v_full[st]);
-            }
-            __syncwarp();
-            loaded = i + 1;
-        }
-        // leave only once the copies in flight have landed
-        if (count > 0) (void)mbar_wait(q_full, 0, f.flags);
-        for (int i = max(0, loaded - NS); i < loaded; ++i) {
-            (void)mbar_wait(&k_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
-            (void)mbar_wait(&v_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
-        }
-    } else if (warp == 9) {
-        // ----------------------------------------------------------------- MMA
-        const uint32_t id_s = umma_idesc<T>(kAmKeys, false, f.negate != 0);
-        const uint32_t id_o = umma_idesc<T>(dvn, true, false);
-        const uint32_t q_s = smem_u32(qs), k_s = smem_u32(ks), v_s = smem_u32(vs);
-        auto scores = [&](int i, int m) {
-            const uint32_t qa = q_s + m * DCH * kAmChunkBytes;
-            const uint32_t kb = k_s + ((i % NS) * 2 + m) * DCH * kAmChunkBytes;
-            for (int k = 0; k < f.dsteps; ++k) {
-                const uint32_t off = (uint32_t)(k >> 2) * kAmChunkBytes + 32 * (k & 3);
-                umma_f16(tmem + m * 128, umma_desc128(qa + off, 16), umma_desc128(kb + off, 16),
-                         id_s, k != 0 ? 1u : 0u);
-            }
-            umma_commit(&s_full[m]);
-        };
-        bool ok = count > 0 && mbar_wait(q_full, 0, f.flags) && mbar_wait(&k_full[0], 0, f.flags);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && lane == 0) {
-            tmem_fence_after();
-            scores(0, 0);
-            scores(0, 1);
-            umma_commit(&k_empty[0]);
-        }
-        for (int i = 0; i < count && ok; ++i) {
-            const int st = i % NS;
-            ok = mbar_wait(&v_full[st], (uint32_t)((i / NS) & 1), f.flags);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            for (int w = 0; w < 4; ++w) {
-                uint32_t hidden = ~vis[st * 4 + w];
-                if (hidden == 0) continue;
-                // 8 lanes a row of a chunk, 4 rows at a time
-                for (int r = lane >> 3; r < 32; r += 4)
-                    if (hidden >> r & 1)
-                        for (int c = 0; c < vch; ++c)
-                            *reinterpret_cast<uint4*>(vs + st * vstage + c * kAmChunkBytes +
-                                                      (w * 32 + r) * 128 + (lane & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-            }
-            fence_async_shared();
-            __syncwarp();
-            for (int m = 0; m < 2 && ok; ++m) {
-                ok = mbar_wait(&p_full[m], (uint32_t)(i & 1), f.flags);
-                if (m == 0 && i + 1 < count)
-                    ok = ok && mbar_wait(&k_full[(i + 1) % NS],
-                                         (uint32_t)(((i + 1) / NS) & 1), f.flags);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    tmem_fence_after();
-                    for (int k = 0; k < kAmKeys / 16; ++k)
-                        umma_f16_ta(tmem + 256 + m * 128, tmem + m * 128 + k * 8,
-                                    umma_desc128(v_s + st * vstage + k * 2048, kAmChunkBytes), id_o,
-                                    (i | k) != 0 ? 1u : 0u);
-                    umma_commit(&o_done[m]);
-                    if (m == 1) umma_commit(&v_empty[st]);
-                    if (i + 1 < count) {
-                        scores(i + 1, m);
-                        if (m == 1) umma_commit(&k_empty[(i + 1) % NS]);
-                    }
-                }
-                __syncwarp();
-            }
-        }
-    } else if (warp < 8) {
+    if (warp < 8) {
         // ------------------------------------------------------------- softmax
         const int m = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane, tok = q0 + row;
-        const uint32_t t_s = tmem + ((uint32_t)(quarter * 32) << 16) + m * 128;
-        const uint32_t t_o = t_s - m * 128 + 256 + m * 128;
+        const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t t_o = t_row + 256 + m * 128;
         const int limit = a.causal ? min(len, tok + len - a.Lq + 1) : len;
         const float sc = a.scale_log2;
         float top = -INFINITY, sum = 0.f;        // reference maximum of the weights, their sum
         bool ok = true;
-        for (int i = 0; i < count; ++i) {
-            const int st = i % NS, j0 = (t0 + i) * kAmKeys;
-            ok = mbar_wait(&s_full[m], (uint32_t)(i & 1), f.flags);
-            if (ok && a.mask) ok = mbar_wait(&v_full[st], (uint32_t)((i / NS) & 1), f.flags);
+        Ring v(NS);
+        for (int i = 0; i < count; ++i, v.next()) {
+            const int st = v.st, buf = m * 2 + (i & 1), j0 = (t0 + i) * kAmKeys;
+            const uint32_t t_s = t_row + buf * 64;
+            ok = mbar_wait(&s_full[buf], (uint32_t)((i >> 1) & 1), f.flags);
+            if (ok && a.mask) ok = mbar_wait(&v_full[st], v.phase, f.flags);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
             }
             tmem_fence_after();
-            uint32_t r[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, r + 32 * c);
+            uint32_t r[64];
+            tmem_ld32(t_s, r);
+            tmem_ld32(t_s + 32, r + 32);
             tmem_wait_ld();
             float* s = reinterpret_cast<float*>(r);
             const int cnt = limit - j0;
             if (!__all_sync(0xffffffffu, cnt >= kAmKeys) || a.mask) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t bits = a.mask ? vis[st * 4 + w] : 0xffffffffu;
+                for (int w = 0; w < 2; ++w) {
+                    uint32_t bits = a.mask ? vis[st * 2 + w] : 0xffffffffu;
                     const int in = cnt - 32 * w;
                     bits = in >= 32 ? bits : in <= 0 ? 0u : bits & ((1u << in) - 1u);
 #pragma unroll
@@ -291,13 +195,15 @@ __global__ void __launch_bounds__(kAmThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) mx[c] = s[c];
 #pragma unroll
-            for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+            for (int c = 4; c < kAmKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
             const float hi = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc - kBias;
             const bool first = top == -INFINITY;
             const bool grow = !first && hi > top + kAmLazy;
             if (__any_sync(0xffffffffu, grow)) {
-                // the last value product has to be in O_m
-                ok = __all_sync(0xffffffffu, mbar_wait(&o_done[m], (uint32_t)((i - 1) & 1), f.flags));
+                // the last value product has to be in O_m (the one before it is: S_m(i) went
+                // out after it)
+                ok = mbar_wait(&o_done[buf ^ 1], (uint32_t)(((i - 1) >> 1) & 1), f.flags);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tmem_fence_after();
                 const float keep = grow ? ex2(top - hi) : 1.f;
@@ -317,31 +223,29 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             const float ref = top == -INFINITY ? 0.f : top;
             const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t p[32];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const int at = 64 * h + 2 * c;
-                    float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), sc2, rf2);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    acc[c & 1] = __fadd2_rn(acc[c & 1], x);
-                    p[c] = Elem<T>::pack2(x.x, x.y);
-                }
-                tmem_st32(t_s + 32 * h, p);
+            for (int c = 0; c < 32; ++c) {
+                float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sc2, rf2);
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                acc[c & 1] = __fadd2_rn(acc[c & 1], x);
+                p[c] = Elem<T>::pack2(x.x, x.y);
             }
+            tmem_st32(t_s, p);
             sum += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[m]);
+            if (lane == 0) mbar_arrive(&p_full[buf]);
         }
         // ------------------------------------------------------------ epilogue
-        if (ok && count > 0) {
-            ok = mbar_wait(&o_done[0], (uint32_t)((count - 1) & 1), f.flags);
-            ok = mbar_wait(&o_done[1], (uint32_t)((count - 1) & 1), f.flags) && ok;
+        if (count > 0) {
+            const int b = (count - 1) & 1;
+            const uint32_t ph = (uint32_t)(((count - 1) >> 1) & 1);
+            ok = ok && mbar_wait(&o_done[b], ph, f.flags) && mbar_wait(&o_done[2 + b], ph, f.flags);
         }
+        __syncwarp();
         tmem_fence_after();
         inv[m * 128 + row] = sum > 0.f ? 1.f / sum : 0.f;
         const bool live = tok < a.Lq;
@@ -363,13 +267,12 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         named_barrier(1, 256);
         const float i0 = inv[row], i1 = inv[128 + row];
         const float lam = Elem<T>::one(static_cast<const T*>(a.lam) + head);
-        const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16) + 256;
         const long long to = (((long long)n * a.Lq + tok) * a.M + head) * a.Dv + c0;
         for (int c = 16 * m; c < dvn; c += 32) {
             uint32_t o0[16], o1[16];
             if (count > 0) {
-                tmem_ld16(t_row + c, o0);
-                tmem_ld16(t_row + 128 + c, o1);
+                tmem_ld16(t_row + 256 + c, o0);
+                tmem_ld16(t_row + 384 + c, o1);
                 tmem_wait_ld();
             } else {
 #pragma unroll
@@ -400,6 +303,131 @@ __global__ void __launch_bounds__(kAmThreads, 1)
                     }
             }
             __syncwarp();
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ producer
+        bool ok = true;
+        int loaded = 0;
+        if (count > 0 && lane == 0) {
+            mbar_arrive_expect_tx(q_full, (uint32_t)(2 * DCH * kAmQBytes));
+            for (int m = 0; m < 2; ++m)
+                for (int c = 0; c < DCH; ++c)
+                    tma_load_4d(qs + (m * DCH + c) * kAmQBytes, &f.tq, c * 64, head * 2 + m, q0, n,
+                                q_full);
+        }
+        Ring v(NS);
+        for (int i = 0; i < count; ++i, v.next()) {
+            const int st = v.st, j0 = (t0 + i) * kAmKeys;
+            const uint32_t ph = v.phase ^ 1;
+            if (i >= NS) ok = mbar_wait(&k_empty[st], ph, f.flags);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&k_full[st], (uint32_t)(2 * DCH * kAmKBytes));
+                for (int m = 0; m < 2; ++m)
+                    for (int c = 0; c < DCH; ++c)
+                        tma_load_4d(ks + ((st * 2 + m) * DCH + c) * kAmKBytes, &f.tk, c * 64,
+                                    kv * 2 + m, j0, n, &k_full[st]);
+            }
+            if (i >= NS) ok = mbar_wait(&v_empty[st], ph, f.flags);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            for (int w = 0; w < 2; ++w) {
+                const uint32_t bits = attn_key_bits(a, n, j0 + 32 * w, len, lane);
+                if (lane == 0) vis[st * 2 + w] = bits;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&v_full[st], (uint32_t)(vch * kAmKBytes));
+                for (int c = 0; c < vch; ++c)
+                    tma_load_4d(vs + st * vstage + c * kAmKBytes, &f.tv, c0 + c * 64, kv, j0, n,
+                                &v_full[st]);
+            }
+            __syncwarp();
+            loaded = i + 1;
+        }
+        // leave only once the copies in flight have landed
+        if (count > 0) (void)mbar_wait(q_full, 0, f.flags);
+        for (int i = max(0, loaded - NS); i < loaded; ++i) {
+            (void)mbar_wait(&k_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
+            (void)mbar_wait(&v_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
+        }
+    } else {
+        // ----------------------------------------------------------------- MMA
+        const uint32_t id_s = umma_idesc<T>(kAmKeys, false, f.negate != 0);
+        const uint32_t id_o = umma_idesc<T>(dvn, true, false);
+        const uint32_t q_s = smem_u32(qs), k_s = smem_u32(ks), v_s = smem_u32(vs);
+        // descriptors: the start address and the leading offset in the low word
+        const uint32_t d_hi = (uint32_t)(umma_desc128(0, 0) >> 32);
+        const uint32_t lo_k = 16u >> 4 << 16, lo_v = (uint32_t)kAmKBytes >> 4 << 16;
+        // S_m of the key stage st to its buffer; the key tile is free after map 1's
+        auto scores = [&](int st, int buf, int m) {
+            const uint32_t qa = ((q_s + m * DCH * kAmQBytes) >> 4) + lo_k;
+            const uint32_t kb = ((k_s + (st * 2 + m) * DCH * kAmKBytes) >> 4) + lo_k;
+#pragma unroll
+            for (int k = 0; k < 4 * DCH; ++k)
+                if (k < f.dsteps)
+                    umma_f16(tmem + buf * 64,
+                             umma_desc_of(qa + (k >> 2) * (kAmQBytes >> 4) + 2 * (k & 3), d_hi),
+                             umma_desc_of(kb + (k >> 2) * (kAmKBytes >> 4) + 2 * (k & 3), d_hi),
+                             id_s, k != 0 ? 1u : 0u);
+            umma_commit(&s_full[buf]);
+            if (m == 1) umma_commit(&k_empty[st]);
+        };
+        bool ok = count > 0 && mbar_wait(q_full, 0, f.flags);
+        Ring kr(NS), v(NS);
+        for (int i = 0; i < min(2, count); ++i, kr.next()) {
+            ok = ok && mbar_wait(&k_full[kr.st], kr.phase, f.flags);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && elect_one()) {
+                tmem_fence_after();
+                scores(kr.st, i, 0);
+                scores(kr.st, 2 + i, 1);
+            }
+            __syncwarp();
+        }
+        for (int i = 0; i < count && ok; ++i, v.next(), kr.next()) {
+            const int st = v.st;
+            ok = mbar_wait(&v_full[st], v.phase, f.flags);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t vis0 = vis[st * 2], vis1 = vis[st * 2 + 1];
+            if ((vis0 & vis1) != 0xffffffffu) {
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t hidden = ~(w ? vis1 : vis0);
+                    // 8 lanes a row of a chunk, 4 rows at a time
+                    for (int r = lane >> 3; r < 32; r += 4)
+                        if (hidden >> r & 1)
+                            for (int c = 0; c < vch; ++c)
+                                *reinterpret_cast<uint4*>(vs + st * vstage + c * kAmKBytes +
+                                                          (w * 32 + r) * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                }
+                fence_async_shared();
+                __syncwarp();
+            }
+            const uint32_t vb = ((v_s + st * vstage) >> 4) + lo_v;
+            const uint32_t ph = (uint32_t)((i >> 1) & 1);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int buf = m * 2 + (i & 1);
+                ok = ok && mbar_wait(&p_full[buf], ph, f.flags);
+                if (m == 0 && i + 2 < count)
+                    ok = ok && mbar_wait(&k_full[kr.st], kr.phase, f.flags);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    tmem_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kAmKeys / 16; ++k)
+                        umma_f16_ta(tmem + 256 + m * 128, tmem + buf * 64 + k * 8,
+                                    umma_desc_of(vb + k * (2048 >> 4), d_hi), id_o,
+                                    (i | k) != 0 ? 1u : 0u);
+                    umma_commit(&o_done[buf]);
+                    if (m == 1) umma_commit(&v_empty[st]);
+                    if (i + 2 < count) scores(kr.st, buf, m);
+                }
+                __syncwarp();
+            }
         }
     }
     tmem_fence_before();

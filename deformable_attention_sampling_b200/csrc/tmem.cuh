@@ -16,6 +16,23 @@ __device__ __forceinline__ uint64_t umma_desc128(uint32_t smem_addr, uint32_t lb
            ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
+// A descriptor from its two words: the start address lies in the low one, in
+// units of 16 bytes, so a tile's descriptors differ by small sums.
+__device__ __forceinline__ uint64_t umma_desc_of(uint32_t lo, uint32_t hi) {
+    return (uint64_t)hi << 32 | lo;
+}
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Instruction descriptor of kind::f16 with a float32 accumulator, M = 128:
 // `mn_b`: B is MN-major; `neg_a`: the product is taken with -A.
 template <typename T>

@@ -13,6 +13,13 @@ DEV = "cuda:0"
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 
 
+@pytest.fixture(autouse=True)
+def no_wait_ran_out():
+    yield
+    torch.cuda.synchronize()
+    assert dcnb.dcn_device_flags(reset=True) == 0
+
+
 def inputs(N, Lq, Lk, M, Mk, D, Dv, dtype, seed=0):
     g = torch.Generator().manual_seed(seed)
     n = (lambda *s, std=1.0, mean=0.0: (torch.randn(s, generator=g) * std + mean).to(dtype).to(DEV))
