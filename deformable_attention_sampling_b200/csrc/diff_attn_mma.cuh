@@ -2,19 +2,20 @@
 // forward, 16-bit types (sm_100a).  The mathematics is diff_attn.cuh's.
 //
 // One CTA owns 128 tokens of one head and walks the keys in tiles of 64, with
-// both softmax maps in flight and two score buffers a map: the tensor cores run
-// up to two tiles ahead, so that the softmax warps find their next scores ready.
-//   producer (one thread)   tensor-map loads of the tokens' two query tiles,
+// both softmax maps in flight, each with its own issuing warp:
+//   producer (one warp)     tensor-map loads of the tokens' two query tiles,
 //             then per tile the two key tiles and the value tile (128-byte
 //             swizzle, rows past the tensor read as zeros);
-//   MMA       (one thread)  S_m = Q_m K_m^T (float32, 64 TMEM columns a buffer)
-//             and O_m += P_m V, P_m as the left operand from TMEM, V from the
+//   MMA       (a warp a map)  S_m = Q_m K_m^T (float32, 64 TMEM columns), and
+//             O_m += P_m V, P_m as the left operand from TMEM, V from the
 //             shared tile as it lies (N-major);
 //   softmax   (four warps a map, thread = token) reads its row of S_m, keeps
-//             the running maximum and sum, writes P_m in 16 bits over S_m.
-// TMEM: S_0, S_1 two buffers of 64 columns each, O_0, O_1 up to 128 columns
-// each: all 512.  The products of one CTA run in the order of their issue:
-// S_m(i + 2) goes out after P_m(i) V, whose left operand it overwrites.
+//             the running maximum and sum, writes P_m in 16 bits;
+//   cleaner   (one warp)     zeroes the value rows of hidden keys.
+// S_m(i + 1) is computed as soon as the softmax warps hold S_m(i) in registers,
+// while they work on it; P_m has two buffers, so that they do not wait for the
+// value product either.  TMEM: a map's scores 64 columns and weights 2 x 32,
+// O_0, O_1 up to 128 columns each: all 512.
 //
 // The running maximum is lowered into O only when it has grown by more than
 // 2^8 (the weights stay below 2^8 then, or 2^14 with fp16's bias): O_m lives in
@@ -23,9 +24,9 @@
 // the largest stay normal numbers.  Weights enter the product rounded to the
 // type (half a step of the type each), their sum is that of the unrounded ones.
 //
-// Keys that no token may see (past the length, masked) get weight 0, and the
-// MMA warp zeroes their value rows in the tile first: 0 times what lies there
-// must not be NaN.
+// Keys that no token may see (past the length, masked) get weight 0, and their
+// value rows are zeroed in the tile first: 0 times what lies there must not be
+// NaN.
 //
 // Bound: per 128 x 64 tile and map the exponentials take 512 cycles of the
 // special-function units and the products 384 (D = 64, Dv = 128).
@@ -38,7 +39,7 @@ namespace dcnb {
 
 constexpr int kAmRows = 128;                 // tokens of a CTA
 constexpr int kAmKeys = 64;                  // keys of a tile
-constexpr int kAmThreads = 320;              // 2 x 4 softmax warps, producer, MMA
+constexpr int kAmThreads = 384;              // 2 x 4 softmax warps, producer, 2 MMA, cleaner
 constexpr int kAmQBytes = kAmRows * 128;     // 64 columns of the query tile, of a
 constexpr int kAmKBytes = kAmKeys * 128;     // key or value tile (16-bit elements)
 constexpr int kAmMaxDv = 128;                // value columns of a CTA
@@ -121,23 +122,31 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     uint64_t* k_empty = k_full + NS;
     uint64_t* v_full = k_empty + NS;
     uint64_t* v_empty = v_full + NS;
-    uint64_t* s_full = v_empty + NS;      // [map][buffer] scores written
-    uint64_t* p_full = s_full + 4;        // [map][buffer] weights written
+    uint64_t* v_clean = v_empty + NS;     // value tile ready, hidden rows zeroed
+    uint64_t* s_full = v_clean + NS;      // [map] scores written
+    uint64_t* s_free = s_full + 2;        // [map] scores read
+    uint64_t* p_full = s_free + 2;        // [map][buffer] weights written
     uint64_t* o_done = p_full + 4;        // [map][buffer] value product done
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 4);
+    uint64_t* lead_off = o_done + 4;      // map 0 has its first weights
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(lead_off + 1);
     uint32_t* vis = tmem_slot + 4;                                // [NS][2] key bits of a tile
     float* inv = reinterpret_cast<float*>(vis + NS * 2);          // [2][128]
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
+        mbar_init(lead_off, 4);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&k_full[s], 1);
-            mbar_init(&k_empty[s], 1);
+            mbar_init(&k_empty[s], 2);
             mbar_init(&v_full[s], 1);
-            mbar_init(&v_empty[s], 1);
+            mbar_init(&v_empty[s], 2);
+            mbar_init(&v_clean[s], 1);
+        }
+        for (int m = 0; m < 2; ++m) {
+            mbar_init(&s_full[m], 1);
+            mbar_init(&s_free[m], 4);
         }
         for (int m = 0; m < 4; ++m) {
-            mbar_init(&s_full[m], 1);
             mbar_init(&p_full[m], 4);
             mbar_init(&o_done[m], 1);
         }
@@ -158,27 +167,36 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         const int m = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane, tok = q0 + row;
         const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t t_o = t_row + 256 + m * 128;
+        const uint32_t t_s = t_row + m * 128, t_o = t_row + 256 + m * 128;
         const int limit = a.causal ? min(len, tok + len - a.Lq + 1) : len;
         const float sc = a.scale_log2;
         float top = -INFINITY, sum = 0.f;        // reference maximum of the weights, their sum
         bool ok = true;
-        Ring v(NS);
-        for (int i = 0; i < count; ++i, v.next()) {
-            const int st = v.st, buf = m * 2 + (i & 1), j0 = (t0 + i) * kAmKeys;
-            const uint32_t t_s = t_row + buf * 64;
-            ok = mbar_wait(&s_full[buf], (uint32_t)((i >> 1) & 1), f.flags);
-            if (ok && a.mask) ok = mbar_wait(&v_full[st], v.phase, f.flags);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+        uint32_t r[64];
+        float* s = reinterpret_cast<float*>(r);
+        // The scores of tile i on their way to registers.  Their barrier counts every product
+        // that map's warp issued before: the weights of tile i - 2 have been read, too.
+        auto fetch = [&](int i) {
+            ok = mbar_wait(&s_full[m], (uint32_t)(i & 1), f.flags);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
             tmem_fence_after();
-            uint32_t r[64];
             tmem_ld32(t_s, r);
             tmem_ld32(t_s + 32, r + 32);
+        };
+        if (count > 0) fetch(0);
+        Ring v(NS);
+        for (int i = 0; i < count && ok; ++i, v.next()) {
+            const int st = v.st, buf = m * 2 + (i & 1), j0 = (t0 + i) * kAmKeys;
+            if (a.mask) {          // its key bits
+                ok = mbar_wait(&v_full[st], v.phase, f.flags);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
             tmem_wait_ld();
-            float* s = reinterpret_cast<float*>(r);
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[m]);
             const int cnt = limit - j0;
             if (!__all_sync(0xffffffffu, cnt >= kAmKeys) || a.mask) {
 #pragma unroll
@@ -193,15 +211,15 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             }
             float mx[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) mx[c] = s[c];
+            for (int c = 0; c < 4; ++c) mx[c] = max3(s[3 * c], s[3 * c + 1], s[3 * c + 2]);
 #pragma unroll
-            for (int c = 4; c < kAmKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-            const float hi = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc - kBias;
+            for (int c = 12; c + 1 < kAmKeys; c += 2)
+                mx[c / 2 & 3] = max3(mx[c / 2 & 3], s[c], s[c + 1]);
+            const float hi = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sc - kBias;
             const bool first = top == -INFINITY;
             const bool grow = !first && hi > top + kAmLazy;
             if (__any_sync(0xffffffffu, grow)) {
-                // the last value product has to be in O_m (the one before it is: S_m(i) went
-                // out after it)
+                // the last value product has to be in O_m
                 ok = mbar_wait(&o_done[buf ^ 1], (uint32_t)(((i - 1) >> 1) & 1), f.flags);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -232,12 +250,16 @@ __global__ void __launch_bounds__(kAmThreads, 1)
                 acc[c & 1] = __fadd2_rn(acc[c & 1], x);
                 p[c] = Elem<T>::pack2(x.x, x.y);
             }
-            tmem_st32(t_s, p);
+            tmem_st32(t_s + 64 + 32 * (i & 1), p);
+            if (i + 1 < count) fetch(i + 1);
             sum += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[buf]);
+            if (lane == 0) {
+                mbar_arrive(&p_full[buf]);
+                if (m == 0 && i == 0) mbar_arrive(lead_off);
+            }
         }
         // ------------------------------------------------------------ epilogue
         if (count > 0) {
@@ -351,45 +373,77 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             (void)mbar_wait(&k_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
             (void)mbar_wait(&v_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
         }
-    } else {
-        // ----------------------------------------------------------------- MMA
+    } else if (warp < 11) {
+        // ------------------------------------------------------- MMA of one map
+        const int m = warp - 9;
         const uint32_t id_s = umma_idesc<T>(kAmKeys, false, f.negate != 0);
         const uint32_t id_o = umma_idesc<T>(dvn, true, false);
-        const uint32_t q_s = smem_u32(qs), k_s = smem_u32(ks), v_s = smem_u32(vs);
         // descriptors: the start address and the leading offset in the low word
         const uint32_t d_hi = (uint32_t)(umma_desc128(0, 0) >> 32);
         const uint32_t lo_k = 16u >> 4 << 16, lo_v = (uint32_t)kAmKBytes >> 4 << 16;
-        // S_m of the key stage st to its buffer; the key tile is free after map 1's
-        auto scores = [&](int st, int buf, int m) {
-            const uint32_t qa = ((q_s + m * DCH * kAmQBytes) >> 4) + lo_k;
+        const uint32_t qa = ((smem_u32(qs) + m * DCH * kAmQBytes) >> 4) + lo_k;
+        const uint32_t k_s = smem_u32(ks), v_s = smem_u32(vs);
+        const uint32_t t_s = tmem + m * 128, t_o = tmem + 256 + m * 128;
+        auto scores = [&](int st) {
             const uint32_t kb = ((k_s + (st * 2 + m) * DCH * kAmKBytes) >> 4) + lo_k;
 #pragma unroll
             for (int k = 0; k < 4 * DCH; ++k)
                 if (k < f.dsteps)
-                    umma_f16(tmem + buf * 64,
+                    umma_f16(t_s,
                              umma_desc_of(qa + (k >> 2) * (kAmQBytes >> 4) + 2 * (k & 3), d_hi),
                              umma_desc_of(kb + (k >> 2) * (kAmKBytes >> 4) + 2 * (k & 3), d_hi),
                              id_s, k != 0 ? 1u : 0u);
-            umma_commit(&s_full[buf]);
-            if (m == 1) umma_commit(&k_empty[st]);
+            umma_commit(&s_full[m]);
+            umma_commit(&k_empty[st]);
         };
-        bool ok = count > 0 && mbar_wait(q_full, 0, f.flags);
         Ring kr(NS), v(NS);
-        for (int i = 0; i < min(2, count); ++i, kr.next()) {
-            ok = ok && mbar_wait(&k_full[kr.st], kr.phase, f.flags);
+        bool ok = count > 0 && mbar_wait(q_full, 0, f.flags) && mbar_wait(&k_full[0], 0, f.flags);
+        // half a tile apart, the maps' warps take turns at the exponentials
+        if (m == 1) ok = ok && mbar_wait(lead_off, 0, f.flags);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && elect_one()) {
+            tmem_fence_after();
+            scores(0);
+        }
+        __syncwarp();
+        kr.next();
+        for (int i = 0; i < count && ok; ++i, v.next(), kr.next()) {
+            const int st = v.st, buf = m * 2 + (i & 1);
+            if (i + 1 < count) {
+                ok = mbar_wait(&k_full[kr.st], kr.phase, f.flags) &&
+                     mbar_wait(&s_free[m], (uint32_t)(i & 1), f.flags);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (elect_one()) {
+                    tmem_fence_after();
+                    scores(kr.st);
+                }
+                __syncwarp();
+            }
+            ok = mbar_wait(&v_clean[st], v.phase, f.flags) &&
+                 mbar_wait(&p_full[buf], (uint32_t)((i >> 1) & 1), f.flags);
             ok = __all_sync(0xffffffffu, ok);
-            if (ok && elect_one()) {
+            if (!ok) break;
+            if (elect_one()) {
                 tmem_fence_after();
-                scores(kr.st, i, 0);
-                scores(kr.st, 2 + i, 1);
+                const uint32_t vb = ((v_s + st * vstage) >> 4) + lo_v;
+                const uint32_t t_p = t_s + 64 + 32 * (i & 1);
+#pragma unroll
+                for (int k = 0; k < kAmKeys / 16; ++k)
+                    umma_f16_ta(t_o, t_p + k * 8, umma_desc_of(vb + k * (2048 >> 4), d_hi), id_o,
+                                (i | k) != 0 ? 1u : 0u);
+                umma_commit(&o_done[buf]);
+                umma_commit(&v_empty[st]);
             }
             __syncwarp();
         }
-        for (int i = 0; i < count && ok; ++i, v.next(), kr.next()) {
+    } else {
+        // ------------------------------------------------------------- cleaner
+        Ring v(NS);
+        for (int i = 0; i < count; ++i, v.next()) {
             const int st = v.st;
-            ok = mbar_wait(&v_full[st], v.phase, f.flags);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            const bool ok = mbar_wait(&v_full[st], v.phase, f.flags);
+            if (!__all_sync(0xffffffffu, ok)) break;
             const uint32_t vis0 = vis[st * 2], vis1 = vis[st * 2 + 1];
             if ((vis0 & vis1) != 0xffffffffu) {
                 for (int w = 0; w < 2; ++w) {
@@ -405,29 +459,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
                 fence_async_shared();
                 __syncwarp();
             }
-            const uint32_t vb = ((v_s + st * vstage) >> 4) + lo_v;
-            const uint32_t ph = (uint32_t)((i >> 1) & 1);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int buf = m * 2 + (i & 1);
-                ok = ok && mbar_wait(&p_full[buf], ph, f.flags);
-                if (m == 0 && i + 2 < count)
-                    ok = ok && mbar_wait(&k_full[kr.st], kr.phase, f.flags);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (elect_one()) {
-                    tmem_fence_after();
-#pragma unroll
-                    for (int k = 0; k < kAmKeys / 16; ++k)
-                        umma_f16_ta(tmem + 256 + m * 128, tmem + buf * 64 + k * 8,
-                                    umma_desc_of(vb + k * (2048 >> 4), d_hi), id_o,
-                                    (i | k) != 0 ? 1u : 0u);
-                    umma_commit(&o_done[buf]);
-                    if (m == 1) umma_commit(&v_empty[st]);
-                    if (i + 2 < count) scores(kr.st, buf, m);
-                }
-                __syncwarp();
-            }
+            if (lane == 0) mbar_arrive(&v_clean[st]);
         }
     }
     tmem_fence_before();
