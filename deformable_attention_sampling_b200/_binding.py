@@ -72,7 +72,7 @@ SIGNATURES = {
     "diff_attn_forward_workspace_size": (_LL, [_I] * 8),
     "diff_attn_forward": (_I, [_VP] * 10 + [_LL] + [_I] * 7 + [_LL] * 6 +
                           [ctypes.c_float, _I, _I, _VP]),
-    "diff_attn_backward_workspace_size": (_LL, [_I] * 4),
+    "diff_attn_backward_workspace_size": (_LL, [_I] * 8),
     "diff_attn_backward": (_I, [_VP] * 15 + [_LL] + [_I] * 7 + [_LL] * 6 +
                            [ctypes.c_float, _I, _I, _VP]),
     "dcn_output_size": (_I, [_I] * 5),
@@ -385,8 +385,8 @@ def diff_attn_forward(q, k, v, lam, mask, lengths, out, out2, lse, workspace, wo
         "diff_attn_forward")
 
 
-def diff_attn_backward_workspace_size(N, Lq, M, dtype):
-    return int(_load().diff_attn_backward_workspace_size(N, Lq, M, dtype))
+def diff_attn_backward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype):
+    return int(_load().diff_attn_backward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype))
 
 
 def diff_attn_backward(q, k, v, lam, mask, lengths, out, out2, lse, grad_out, grad_q, grad_k,
@@ -893,7 +893,7 @@ def diff_attn_grad(q, k, v, lam, out, saved, grad_out, mask=None, lengths=None, 
     gv = torch.empty((N, Lk, Mk, Dv), dtype=q.dtype, device=q.device)
     gl = torch.empty_like(lam)
     with _on_device(q):
-        need = diff_attn_backward_workspace_size(N, Lq, M, code)
+        need = diff_attn_backward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, code)
         if need < 0:
             raise DcnError(need, "diff_attn_backward_workspace_size")
         ws, ws_bytes = _workspace(need, q.device, workspace)

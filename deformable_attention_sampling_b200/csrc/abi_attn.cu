@@ -3,6 +3,7 @@
 #include "abi_common.cuh"
 #include "diff_attn.cuh"
 #include "diff_attn_mma.cuh"
+#include "diff_attn_mma_bwd.cuh"
 
 using namespace dcnb_abi;
 
@@ -257,6 +258,60 @@ int mma_splits(int N, int Lq, int Lk, int M, int Dv) {
 // Tokens from which the 128-row tiles of the tensor-core forward are taken.
 constexpr int kMmaMinTokens = 17;
 
+// The gradient kernels' tensor-core form: heads and values that its TMEM holds.
+bool mma_bwd_sizes(int dtype, int Lq, int Lk, int D, int Dv) {
+    return mma_sizes(dtype, D, Dv) && D <= dcnb::kAbMaxD && Dv <= dcnb::kAbMaxDv &&
+           Lq >= kMmaMinTokens && Lk > 0;
+}
+
+long long rowv_floats(int N, int Lq, int M) {
+    return (long long)N * M * ceil_div(Lq, dcnb::kRowvTile) * 4 * dcnb::kRowvTile;
+}
+
+int mma_backward(const dcnb::AttnArgs& a, const float* scales, int dtype, void* stream) {
+    dcnb::AttnBwdArgs f;
+    f.a = a;
+    f.negate = a.scale < 0.f ? 1 : 0;
+    f.a.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-30f);
+    f.scales = scales;
+    f.flags = device_flags_word();
+    f.dsteps = ceil_div(a.D, 16);
+    f.vsteps = ceil_div(a.Dv, 16);
+    const int vch = ceil_div(a.Dv, 64);
+    const bool bf16 = dtype == DCN_BF16;
+    const long long g_row = (long long)a.M * a.Dv;
+    // query tiles of 128 tokens over key tiles of 64, then the other way round
+    for (int pass = 0; pass < 2; ++pass) {
+        const int qb = pass == 0 ? dcnb::kAmRows : dcnb::kAmKeys;
+        const int kb = pass == 0 ? dcnb::kAmKeys : dcnb::kAmRows;
+        if (!head_map(&f.tq, a.q, dtype, a.D, 2 * a.M, a.Lq, a.N, a.q_row, a.q_image, qb) ||
+            !head_map(&f.tg, a.go, dtype, a.Dv, a.M, a.Lq, a.N, g_row, g_row * a.Lq, qb) ||
+            !head_map(&f.tk, a.k, dtype, a.D, 2 * a.Mk, a.Lk, a.N, a.k_row, a.k_image, kb) ||
+            !head_map(&f.tv, a.v, dtype, a.Dv, a.Mk, a.Lk, a.N, a.v_row, a.v_image, kb))
+            return DCN_ERR_UNSUPPORTED;
+        f.heads = a.N * (pass == 0 ? a.M : a.Mk);
+        const long long blocks =
+            (long long)ceil_div(pass == 0 ? a.Lq : a.Lk, dcnb::kAmRows) * f.heads;
+        if (blocks > kInt31) return DCN_ERR_UNSUPPORTED;
+        const void* fn;
+        int smem;
+        if (pass == 0) {
+            f.stages = 4;
+            smem = dcnb::attn_dq_smem(vch, f.stages);
+            fn = bf16 ? (const void*)dcnb::diff_attn_dq_mma_kernel<__nv_bfloat16>
+                      : (const void*)dcnb::diff_attn_dq_mma_kernel<__half>;
+        } else {
+            f.stages = 3;
+            smem = dcnb::attn_dkv_smem(vch, f.stages);
+            fn = bf16 ? (const void*)dcnb::diff_attn_dkv_mma_kernel<__nv_bfloat16>
+                      : (const void*)dcnb::diff_attn_dkv_mma_kernel<__half>;
+        }
+        const int rc = launch_attn(fn, f, dim3((unsigned)blocks), dcnb::kAmThreads, smem, stream);
+        if (rc != DCN_OK) return rc;
+    }
+    return DCN_OK;
+}
+
 template <typename T>
 const void* mma_kernel(int dchunks) {
     return dchunks == 1 ? (const void*)dcnb::diff_attn_mma_kernel<T, 1>
@@ -372,9 +427,18 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
     return launch_attn(join, a, dim3((unsigned)((rows_total + 7) / 8)), 256, 0, stream);
 }
 
-long long diff_attn_backward_workspace_size(int N, int Lq, int M, int dtype) {
-    if (elem_bytes(dtype) == 0 || N < 0 || Lq < 0 || M <= 0) return DCN_ERR_INVALID_ARG;
-    return (long long)N * M * 2 * Lq * 4;
+long long diff_attn_backward_workspace_size(int N, int Lq, int Lk, int M, int Mk, int D, int Dv,
+                                            int dtype) {
+    dcnb::AttnArgs a = {};
+    const long long qd = 2LL * M * D, kd = 2LL * Mk * D, vd = (long long)Mk * Dv;
+    const int st = attn_setup(&a, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, N, Lq, Lk,
+                              M, Mk, D, Dv, 0, qd, 0, kd, 0, vd, 1.f, 0, dtype);
+    if (st != DCN_OK) return st;
+    // row values, the two scales (16 bytes), the blocks' peaks of the scaled fp16 kernels
+    long long floats = rowv_floats(N, Lq, M) + 4;
+    if (dtype == DCN_F16 && mma_bwd_sizes(dtype, Lq, Lk, D, Dv))
+        floats += rowv_floats(N, Lq, M) / 32 + ((long long)N * Lk * Mk + 7) / 8;
+    return floats * 4;
 }
 
 int diff_attn_backward(const void* q, const void* k, const void* v, const void* lambda,
@@ -401,7 +465,7 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
          (uintptr_t)grad_k | (uintptr_t)grad_v | (uintptr_t)grad_lambda) % es != 0 ||
         ((uintptr_t)lse | (uintptr_t)lengths) % 4 != 0 || (uintptr_t)workspace % 16 != 0)
         return DCN_ERR_MISALIGNED;
-    const long long need = diff_attn_backward_workspace_size(N, Lq, M, dtype);
+    const long long need = diff_attn_backward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype);
     if (workspace_bytes < need) return DCN_ERR_INVALID_ARG;
     const long long ob = tokens * M * Dv * es, sb = tokens * M * 2 * 4;
     Span ins[kInputs + 4];
@@ -417,7 +481,7 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
     a.vec4 = a.vec4 && (uintptr_t)grad_out % (uintptr_t)(4 * es) == 0;
     a.go = grad_out;
     a.lse = const_cast<float*>(lse);
-    a.delta = static_cast<const float*>(workspace);
+    a.rowv = static_cast<const float*>(workspace);
     a.gq = grad_q;
     a.gk = grad_k;
     a.gv = grad_v;
@@ -443,23 +507,34 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
         default: break;
     }
     if (!dq || !dkv) return DCN_ERR_UNSUPPORTED;
+    const bool mma = mma_bwd_sizes(dtype, Lq, Lk, D, Dv) && tokens > 0 && mma_layout(a) &&
+                     ((uintptr_t)grad_out | (uintptr_t)grad_q | (uintptr_t)grad_k |
+                      (uintptr_t)grad_v) % 16 == 0;
+    float* const ws = static_cast<float*>(workspace);
     dcnb::AttnDeltaArgs d = {};
+    d.a = a;
     d.out = out;
     d.out2 = out2;
     d.go = grad_out;
     d.lam = lambda;
-    d.delta = static_cast<float*>(workspace);
+    d.lse = lse;
+    d.rowv = ws;
+    d.scales = ws + rowv_floats(N, Lq, M);
     d.glam = grad_lambda;
-    d.N = N;
-    d.Lq = Lq;
-    d.M = M;
-    d.Dv = Dv;
+    const long long g_blocks = rowv_floats(N, Lq, M) / (4 * 8);
+    const long long v_blocks = mma && dtype == DCN_F16 ? (keys * Mk + 7) / 8 : 0;
+    if (g_blocks + v_blocks > kInt31) return DCN_ERR_UNSUPPORTED;
+    d.g_blocks = (int)g_blocks;
+    d.v_blocks = (int)v_blocks;
+    if (v_blocks > 0) d.peak = d.scales + 4;
     if (tokens > 0) {
-        rc = launch_grid(delta, d, (int)((tokens * M + 7) / 8), 256, 0, stream);
+        rc = launch_grid(delta, d, (int)(g_blocks + v_blocks), 256, 0, stream);
         if (rc != DCN_OK) return rc;
     }
-    rc = launch_grid(glam, d, M, 1024, 0, stream);       // zeros for an empty batch
+    // zeros for an empty batch; one block more for the scales
+    rc = launch_grid(glam, d, mma ? M + 1 : M, 1024, 0, stream);
     if (rc != DCN_OK) return rc;
+    if (mma) return mma_backward(a, d.scales, dtype, stream);
     const int use_ct = bt == 32 && cd <= 4 ? 16 : ct;
     const int smem = dcnb::attn_bwd_smem(bt, cd, use_ct);
     if (tokens > 0) {

@@ -31,6 +31,7 @@ constexpr int kAttnKeys = 64;          // keys of a forward tile
 constexpr int kAttnMaxD = 128;
 constexpr int kAttnMaxDv = 256;
 constexpr int kAttnMaxSplits = 64;
+constexpr int kRowvTile = 64;          // tokens of a tile of row values
 
 struct AttnArgs {
     const void* q;
@@ -46,7 +47,7 @@ struct AttnArgs {
     float* part_o;                 // [splits][N * Mk * rows][2][Dv]
     // gradient
     const void* go;
-    const float* delta;            // [N][M][2][Lq]
+    const float* rowv;             // [N][M][tiles of 64 tokens][4][64]: -lse_0, -lse_1, -e_0, -e_1
     void* gq;
     void* gk;
     void* gv;
@@ -63,6 +64,13 @@ struct AttnArgs {
 
 __device__ __forceinline__ int attn_len(const AttnArgs& a, int n) {
     return a.lengths ? max(0, min(a.lengths[n], a.Lk)) : a.Lk;
+}
+
+// Offset of token tok's first row value (the others follow kRowvTile apart).
+__device__ __forceinline__ long long attn_rowv(const AttnArgs& a, int n, int head, int tok) {
+    const int tiles = (a.Lq + kRowvTile - 1) / kRowvTile;
+    return (((long long)n * a.M + head) * tiles + tok / kRowvTile) * (4 * kRowvTile) +
+           tok % kRowvTile;
 }
 
 // Four elements of a row at column d (D in all) as float32, zeros past the end.
@@ -117,8 +125,8 @@ __device__ __forceinline__ void attn_stage_rows(const AttnArgs& a, const T* base
     }
 }
 
-// Copies key rows [j0, j0 + n) of head kv in the same way; rows whose `ok` flag is 0 (masked or past the end) are
-// zeros, whatever the memory holds.
+// Copies key rows [j0, j0 + n) of head kv in the same way; rows whose `ok` flag is 0
+// (masked or past the end) are zeros, whatever the memory holds.
 template <typename T>
 __device__ __forceinline__ void attn_stage_keys(const AttnArgs& a, const T* base, long long stride,
                                                 int kv, int j0, int n, int parts, int D, float* s,
@@ -431,58 +439,139 @@ struct AttnDeltaArgs {
     const void* out2;
     const void* go;
     const void* lam;
-    float* delta;          // [N][M][2][Lq]: <g, O_0>, <g, O_1>
+    const float* lse;
+    AttnArgs a;            // geometry, visible keys and v
+    float* rowv;
     void* glam;            // second kernel
-    int N, Lq, M, Dv;
+    float* peak;           // [blocks] largest |g|^2 and |v|^2 of a block, or null
+    float* scales;         // cs, cp
+    int g_blocks, v_blocks;
 };
 
-// One warp per (token, head): <g, O_1> from the saved second part, and
-// <g, O_0> = <g, out> + lambda <g, O_1>.
+// One warp per (token, head), tokens padded to whole tiles: e_1 = <g, O_1> from
+// the saved second part, e_0 = <g, O_0> = <g, out> + lambda e_1.  Rows past the
+// end and rows that see no key get -lse = -inf: weights of 0.
+// With `peak` the blocks also find the largest |g|^2 and, in blocks of their
+// own, the largest |v|^2 of a visible key.
 template <typename T>
-__global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArgs a) {
-    const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (at >= (long long)a.N * a.Lq * a.M) return;
-    const T* g = static_cast<const T*>(a.go) + at * a.Dv;
-    const T* o = static_cast<const T*>(a.out) + at * a.Dv;
-    const T* o2 = static_cast<const T*>(a.out2) + at * a.Dv;
-    float s = 0.f, s2 = 0.f;
-    for (int c = lane; c < a.Dv; c += 32) {
-        const float gv = Elem<T>::one(g + c);
-        s = fmaf(gv, Elem<T>::one(o + c), s);
-        s2 = fmaf(gv, Elem<T>::one(o2 + c), s2);
+__global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArgs d) {
+    __shared__ float top[8];
+    const AttnArgs& a = d.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float peak = 0.f;
+    if ((int)blockIdx.x < d.g_blocks) {
+        const int tiles = (a.Lq + kRowvTile - 1) / kRowvTile;
+        const long long at = (long long)blockIdx.x * 8 + warp;
+        const long long tok_all = at / a.M;             // tokens of all images, padded
+        const int h = (int)(at - tok_all * a.M);
+        const int n = (int)(tok_all / (tiles * kRowvTile));
+        const int i = (int)(tok_all - (long long)n * tiles * kRowvTile);
+        if (n < a.N) {
+            float s = 0.f, s2 = 0.f, lse = INFINITY;
+            if (i < a.Lq) {
+                const long long row = (((long long)n * a.Lq + i) * a.M + h) * a.Dv;
+                const T* g = static_cast<const T*>(d.go) + row;
+                const T* o = static_cast<const T*>(d.out) + row;
+                const T* o2 = static_cast<const T*>(d.out2) + row;
+                for (int c = lane; c < a.Dv; c += 32) {
+                    const float gv = Elem<T>::one(g + c);
+                    s = fmaf(gv, Elem<T>::one(o + c), s);
+                    s2 = fmaf(gv, Elem<T>::one(o2 + c), s2);
+                    peak = fmaf(gv, gv, peak);
+                }
+                if (lane < 2) lse = d.lse[(((long long)n * a.M + h) * 2 + lane) * a.Lq + i];
+            }
+            for (int w = 16; w > 0; w >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, w);
+                s2 += __shfl_xor_sync(0xffffffffu, s2, w);
+                peak += __shfl_xor_sync(0xffffffffu, peak, w);
+            }
+            float* r = d.rowv + attn_rowv(a, n, h, i);
+            if (lane < 2) {
+                r[lane * kRowvTile] = -lse;
+                const float lam = Elem<T>::one(static_cast<const T*>(d.lam) + h);
+                r[(2 + lane) * kRowvTile] = lane ? -s2 : -(s + lam * s2);
+            }
+        }
+    } else {
+        const long long at = ((long long)blockIdx.x - d.g_blocks) * 8 + warp;
+        const long long key_all = at / a.Mk;
+        const int kv = (int)(at - key_all * a.Mk), n = (int)(key_all / a.Lk);
+        const int j = (int)(key_all - (long long)n * a.Lk);
+        if (n < a.N && j < attn_len(a, n) && !(a.mask && a.mask[(long long)n * a.Lk + j])) {
+            const T* v = static_cast<const T*>(a.v) + n * a.v_image + (long long)j * a.v_row +
+                         (long long)kv * a.Dv;
+            for (int c = lane; c < a.Dv; c += 32) {
+                const float x = Elem<T>::one(v + c);
+                peak = fmaf(x, x, peak);
+            }
+        }
+        for (int w = 16; w > 0; w >>= 1) peak += __shfl_xor_sync(0xffffffffu, peak, w);
     }
-    for (int w = 16; w > 0; w >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, w);
-        s2 += __shfl_xor_sync(0xffffffffu, s2, w);
-    }
-    if (lane == 0) {
-        const long long tok = at / a.M;
-        const int h = (int)(at - tok * a.M);
-        const long long n = tok / a.Lq, i = tok - n * a.Lq;
-        float* d = a.delta + (n * a.M + h) * 2 * a.Lq + i;
-        d[0] = s + Elem<T>::one(static_cast<const T*>(a.lam) + h) * s2;
-        d[a.Lq] = s2;
+    if (d.peak) {
+        if (lane == 0) top[warp] = peak;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 8; ++w) peak = fmaxf(peak, top[w]);
+            d.peak[blockIdx.x] = peak;
+        }
     }
 }
 
-// grad_lambda of head blockIdx.x: one block, a fixed order.
+// The power of two that brings x to (2^14, 2^15]; 1 for 0, infinities and NaN, and
+// within 2^-40 .. 2^40.
+__device__ __forceinline__ float attn_pow2(float x) {
+    if (!(x > 0.f) || x > 1e30f) return 1.f;
+    return exp2f(fminf(fmaxf(15.f - ceilf(log2f(x)), -40.f), 40.f));
+}
+
+// grad_lambda of head blockIdx.x: one block, a fixed order.  One block more sets
+// the scales of the tensor-core kernels' fp16 operands from the blocks' peaks.
 template <typename T>
-__global__ void __launch_bounds__(1024) diff_attn_glam_kernel(const AttnDeltaArgs a) {
-    __shared__ float part[32];
+__global__ void __launch_bounds__(1024) diff_attn_glam_kernel(const AttnDeltaArgs d) {
+    __shared__ float part[32][3];
+    const AttnArgs& a = d.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((int)blockIdx.x == a.M) {
+        float x[3] = {0.f, 0.f, 0.f};
+        if (d.peak) {
+            for (int i = threadIdx.x; i < d.g_blocks + d.v_blocks; i += 1024) {
+                const int k = i < d.g_blocks ? 0 : 1;
+                x[k] = fmaxf(x[k], d.peak[i]);
+            }
+            for (int h = threadIdx.x; h < a.M; h += 1024)
+                x[2] = fmaxf(x[2], fabsf(Elem<T>::one(static_cast<const T*>(d.lam) + h)));
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            for (int w = 16; w > 0; w >>= 1)
+                x[k] = fmaxf(x[k], __shfl_xor_sync(0xffffffffu, x[k], w));
+            if (lane == 0) part[warp][k] = x[k];
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 32; ++w)
+                for (int k = 0; k < 3; ++k) part[0][k] = fmaxf(part[0][k], part[w][k]);
+            const float lam = part[0][2];
+            // |dS| <= 2 max(1, |lambda|) |g| |v|, |P_0 - lambda P_1| <= 1 + |lambda|
+            d.scales[0] = d.peak ? attn_pow2(2.f * fmaxf(1.f, lam) * sqrtf(part[0][0]) *
+                                             sqrtf(part[0][1])) : 1.f;
+            d.scales[1] = d.peak ? attn_pow2(1.f + lam) : 1.f;
+        }
+        return;
+    }
     const int h = blockIdx.x;
     float s = 0.f;
-    for (int n = 0; n < a.N; ++n) {
-        const float* d = a.delta + (((long long)n * a.M + h) * 2 + 1) * a.Lq;
-        for (int i = threadIdx.x; i < a.Lq; i += 1024) s += d[i];
-    }
+    for (int n = 0; n < a.N; ++n)
+        for (int i = threadIdx.x; i < a.Lq; i += 1024)
+            s += d.rowv[attn_rowv(a, n, h, i) + 3 * kRowvTile];
     for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    if (lane == 0) part[warp][0] = s;
     __syncthreads();
     if (threadIdx.x < 32) {
-        s = part[threadIdx.x];
+        s = part[threadIdx.x][0];
         for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        if (threadIdx.x == 0) static_cast<T*>(a.glam)[h] = Elem<T>::from(-s);
+        if (threadIdx.x == 0) static_cast<T*>(d.glam)[h] = Elem<T>::from(s);
     }
 }
 
@@ -513,25 +602,23 @@ __device__ __forceinline__ AttnBwdTile attn_bwd_tile(float* smem) {
     return t;
 }
 
-// Stages q, g and the five values (lse_0, lse_1, <g, O_0>, <g, O_1>, lambda) of
+// Stages q, g and the five values (-lse_0, -lse_1, -e_0, -e_1, lambda) of
 // packed rows [r0, r0 + BT).
 template <typename T, int BT, int CD, int CT>
-__device__ __forceinline__ void attn_bwd_rows(const AttnArgs& a, const AttnBwdTile& t, int n, int kv,
-                                              int r0) {
+__device__ __forceinline__ void attn_bwd_rows(const AttnArgs& a, const AttnBwdTile& t, int n,
+                                              int kv, int r0) {
     attn_stage_rows<T>(a, static_cast<const T*>(a.q) + n * a.q_image, a.q_row, kv, r0, BT, 2, a.D,
                        t.Qs, 32 * CD + 4, 16 * CD);
     attn_stage_rows<T>(a, static_cast<const T*>(a.go) + (long long)n * a.Lq * a.M * a.Dv,
                        (long long)a.M * a.Dv, kv, r0, BT, 1, a.Dv, t.Gs, attn_ldv(CT), 0);
     for (int i = threadIdx.x; i < BT; i += kAttnThreads) {
-        float v[5] = {INFINITY, INFINITY, 0.f, 0.f, 0.f};
+        float v[5] = {-INFINITY, -INFINITY, 0.f, 0.f, 0.f};
         if (r0 + i < a.rows) {
             const uint32_t tok = a.div_G.div((uint32_t)(r0 + i));
             const int head = kv * a.G + r0 + i - (int)tok * a.G;
-            const long long at = ((long long)n * a.M + head) * 2 * a.Lq + tok;
-            v[0] = a.lse[at];
-            v[1] = a.lse[at + a.Lq];
-            v[2] = a.delta[at];
-            v[3] = a.delta[at + a.Lq];
+            const float* r = a.rowv + attn_rowv(a, n, head, (int)tok);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = r[k * kRowvTile];
             v[4] = Elem<T>::one(static_cast<const T*>(a.lam) + head);
         }
 #pragma unroll
@@ -540,8 +627,8 @@ __device__ __forceinline__ void attn_bwd_rows(const AttnArgs& a, const AttnBwdTi
 }
 
 template <typename T, int BT, int CD, int CT>
-__device__ __forceinline__ void attn_bwd_keys(const AttnArgs& a, const AttnBwdTile& t, int n, int kv,
-                                              int j0, int len) {
+__device__ __forceinline__ void attn_bwd_keys(const AttnArgs& a, const AttnBwdTile& t, int n,
+                                              int kv, int j0, int len) {
     for (int i = threadIdx.x; i < BT; i += kAttnThreads)
         t.ok[i] = j0 + i < len && !(a.mask && a.mask[(long long)n * a.Lk + j0 + i]);
     __syncthreads();
@@ -553,7 +640,7 @@ __device__ __forceinline__ void attn_bwd_keys(const AttnArgs& a, const AttnBwdTi
 
 // The tile's score gradients to S[0], S[1] and, with KEYS, P_0 - lambda P_1 to
 // S[2]; KEYS stores them transposed (key, row).  Rows past the end have
-// lse = +inf, so their probabilities are 0; hidden pairs are exact zeros.
+// -lse = -inf, so their probabilities are 0; hidden pairs are exact zeros.
 template <int BT, int CD, int CT, bool KEYS>
 __device__ __forceinline__ void attn_bwd_scores(const AttnArgs& a, const AttnBwdTile& t, int r0,
                                                 int j0, int len) {
@@ -575,10 +662,10 @@ __device__ __forceinline__ void attn_bwd_scores(const AttnArgs& a, const AttnBwd
         for (int c = 0; c < RT; ++c) {
             const int j = tx + 16 * c;
             const bool see = t.ok[j] && j0 + j < limit;
-            const float p0 = see ? exp2f(t0[r][c] * a.scale_log2 - l0) : 0.f;
-            const float p1 = see ? lam * exp2f(t1[r][c] * a.scale_log2 - l1) : 0.f;
-            const float g0 = see ? p0 * (dp[r][c] - e0) : 0.f;
-            const float g1 = see ? -p1 * (dp[r][c] - e1) : 0.f;
+            const float p0 = see ? exp2f(t0[r][c] * a.scale_log2 + l0) : 0.f;
+            const float p1 = see ? lam * exp2f(t1[r][c] * a.scale_log2 + l1) : 0.f;
+            const float g0 = see ? p0 * (dp[r][c] + e0) : 0.f;
+            const float g1 = see ? -p1 * (dp[r][c] + e1) : 0.f;
             const int at = KEYS ? j * lds + row : row * lds + j;
             t.S[at] = g0;
             t.S[BT * lds + at] = g1;

@@ -639,8 +639,10 @@ DCN_API int diff_attn_forward(const void* q, const void* k, const void* v, const
 DCN_API long long diff_attn_forward_workspace_size(int N, int Lq, int Lk, int M, int Mk, int D,
                                            int Dv, int dtype);
 
-/* Bytes of workspace diff_attn_backward needs. */
-DCN_API long long diff_attn_backward_workspace_size(int N, int Lq, int M, int dtype);
+/* Bytes of workspace diff_attn_backward needs; DCN_ERR_INVALID_ARG or
+ * DCN_ERR_UNSUPPORTED for bad sizes. */
+DCN_API long long diff_attn_backward_workspace_size(int N, int Lq, int Lk, int M, int Mk, int D,
+                                            int Dv, int dtype);
 
 /*
  * diff_attn_backward - gradients of diff_attn_forward with respect to q, k, v
