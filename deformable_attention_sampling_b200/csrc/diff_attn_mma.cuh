@@ -176,15 +176,18 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         float* s = reinterpret_cast<float*>(r);
         // The scores of tile i on their way to registers.  Their barrier counts every product
         // that map's warp issued before: the weights of tile i - 2 have been read, too.
-        auto fetch = [&](int i) {
-            ok = mbar_wait(&s_full[m], (uint32_t)(i & 1), f.flags);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return;
+        // `early`: found complete before (a wait costs 100 cycles even when it is over).
+        auto fetch = [&](int i, bool early) {
+            if (!__all_sync(0xffffffffu, early)) {
+                ok = mbar_wait(&s_full[m], (uint32_t)(i & 1), f.flags);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+            }
             tmem_fence_after();
             tmem_ld32(t_s, r);
             tmem_ld32(t_s + 32, r + 32);
         };
-        if (count > 0) fetch(0);
+        if (count > 0) fetch(0, false);
         Ring v(NS);
         for (int i = 0; i < count && ok; ++i, v.next()) {
             const int st = v.st, buf = m * 2 + (i & 1), j0 = (t0 + i) * kAmKeys;
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             tmem_wait_ld();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free[m]);
+            mbar_arrive_if(lane == 0, &s_free[m]);
             const int cnt = limit - j0;
             if (!__all_sync(0xffffffffu, cnt >= kAmKeys) || a.mask) {
 #pragma unroll
@@ -242,8 +245,10 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             const float2 sc2 = make_float2(sc, sc), rf2 = make_float2(-ref, -ref);
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             uint32_t p[32];
+            bool early = false;
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
+                if (c == 24) early = mbar_test(&s_full[m], (uint32_t)((i + 1) & 1));
                 float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sc2, rf2);
                 x.x = ex2(x.x);
                 x.y = ex2(x.y);
@@ -251,15 +256,13 @@ __global__ void __launch_bounds__(kAmThreads, 1)
                 p[c] = Elem<T>::pack2(x.x, x.y);
             }
             tmem_st32(t_s + 64 + 32 * (i & 1), p);
-            if (i + 1 < count) fetch(i + 1);
+            if (i + 1 < count) fetch(i + 1, early);
             sum += (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&p_full[buf]);
-                if (m == 0 && i == 0) mbar_arrive(lead_off);
-            }
+            mbar_arrive_if(lane == 0, &p_full[buf]);
+            if (m == 0 && i == 0) mbar_arrive_if(lane == 0, lead_off);
         }
         // ------------------------------------------------------------ epilogue
         if (count > 0) {

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             tmem_wait_ld();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s_free);
+            mbar_arrive_if(lane == 0, s_free);
             float* s0 = reinterpret_cast<float*>(r0);
             float* s1 = reinterpret_cast<float*>(r1);
             const float* dp = reinterpret_cast<const float*>(rp);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[b]);
+            mbar_arrive_if(lane == 0, &p_full[b]);
         }
         // (the product before the last was waited for above)
         if (ok && count > 0)
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             tmem_wait_ld();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s_free);
+            mbar_arrive_if(lane == 0, s_free);
             float* s0 = reinterpret_cast<float*>(r0);
             float* s1 = reinterpret_cast<float*>(r1);
             const float* dp = reinterpret_cast<const float*>(rp);
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full);
+            mbar_arrive_if(lane == 0, p_full);
         }
         if (ok && count > 0) ok = mbar_wait(g_done, (uint32_t)((count - 1) & 1), f.flags);
         __syncwarp();
