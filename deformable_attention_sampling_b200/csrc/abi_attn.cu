@@ -4,6 +4,7 @@
 #include "diff_attn.cuh"
 #include "diff_attn_mma.cuh"
 #include "diff_attn_mma_bwd.cuh"
+#include "diff_attn_step.cuh"
 
 using namespace dcnb_abi;
 
@@ -255,6 +256,43 @@ int mma_splits(int N, int Lq, int Lk, int M, int Dv) {
     return (int)std::max(1LL, std::min(s, (long long)dcnb::kAttnMaxSplits));
 }
 
+// The few-token kernel's head and value sizes (D a multiple of 32, so that a
+// lane's quarter is a 16-byte vector; Dv of 32 or more).
+bool step_sizes(int dtype, int D, int Dv) {
+    return dtype != DCN_F32 && (D == 32 || D == 64 || D == 128) &&
+           (Dv == 32 || Dv == 64 || Dv == 128);
+}
+
+// Key splits of the few-token kernel: 3 CTAs of 4 warps a multiprocessor run, and
+// about three rounds of them even out images of different lengths; a split has
+// at least 256 keys.
+int step_splits(int N, int Lq, int Lk, int M, int Mk) {
+    const long long ctas = (long long)ceil_div(Lq * (M / Mk), dcnb::kAsRows) * N * Mk;
+    long long s = (9LL * sm_count() + ctas - 1) / std::max(ctas, 1LL);
+    s = std::min(s, (long long)ceil_div(Lk, 256));
+    return (int)std::max(1LL, std::min(s, (long long)dcnb::kAttnMaxSplits));
+}
+
+template <typename T, int D>
+const void* step_kernel_dv(int Dv) {
+    switch (Dv) {
+        case 32: return (const void*)dcnb::diff_attn_step_kernel<T, D, 32>;
+        case 64: return (const void*)dcnb::diff_attn_step_kernel<T, D, 64>;
+        case 128: return (const void*)dcnb::diff_attn_step_kernel<T, D, 128>;
+        default: return nullptr;
+    }
+}
+
+template <typename T>
+const void* step_kernel(int D, int Dv) {
+    switch (D) {
+        case 32: return step_kernel_dv<T, 32>(Dv);
+        case 64: return step_kernel_dv<T, 64>(Dv);
+        case 128: return step_kernel_dv<T, 128>(Dv);
+        default: return nullptr;
+    }
+}
+
 // Tokens from which the 128-row tiles of the tensor-core forward are taken.
 constexpr int kMmaMinTokens = 17;
 
@@ -366,6 +404,8 @@ long long diff_attn_forward_workspace_size(int N, int Lq, int Lk, int M, int Mk,
     int splits = attn_plan(N, Lq, Lk, M, Mk).splits;
     if (mma_sizes(dtype, D, Dv) && Lq >= kMmaMinTokens)
         splits = std::max(splits, mma_splits(N, Lq, Lk, M, Dv));
+    if (step_sizes(dtype, D, Dv) && Lq < kMmaMinTokens)
+        splits = std::max(splits, step_splits(N, Lq, Lk, M, Mk));
     if (splits == 1) return 0;
     return (long long)splits * N * M * Lq * 2 * (2 + (long long)Dv) * 4;
 }
@@ -390,6 +430,7 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
     const AttnPlan p = attn_plan(N, Lq, Lk, M, Mk);
     const bool mma = mma_sizes(dtype, D, Dv) && Lq >= kMmaMinTokens && mma_layout(a) &&
                      ((uintptr_t)out | (uintptr_t)out2) % 16 == 0;
+    const bool step = step_sizes(dtype, D, Dv) && Lq < kMmaMinTokens && mma_layout(a);
     const long long need = diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return DCN_ERR_INVALID_ARG;
     const long long ob = (long long)N * Lq * M * Dv * es;
@@ -401,7 +442,9 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
     a.out = out;
     a.out2 = out2;
     a.lse = lse;
-    a.splits = mma ? mma_splits(N, Lq, Lk, M, Dv) : p.splits;
+    a.splits = mma    ? mma_splits(N, Lq, Lk, M, Dv)
+               : step ? step_splits(N, Lq, Lk, M, Mk)
+                      : p.splits;
     const long long rows_total = (long long)N * M * Lq;
     if (a.splits > 1) {
         a.part_o = static_cast<float*>(workspace);
@@ -420,9 +463,16 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
         default: break;
     }
     if (!fn) return DCN_ERR_UNSUPPORTED;
-    rc = mma ? mma_forward(a, dtype, stream)
-             : launch_attn(fn, a, dim3(p.tiles, N * Mk, a.splits), dcnb::kAttnThreads,
-                           dcnb::attn_fwd_smem(p.bq, D, ct), stream);
+    if (step) {
+        fn = dtype == DCN_BF16 ? step_kernel<__nv_bfloat16>(D, Dv) : step_kernel<__half>(D, Dv);
+        rc = launch_attn(fn, a, dim3(ceil_div(a.rows, dcnb::kAsRows), N * Mk, a.splits),
+                         dcnb::kAsThreads, dcnb::attn_step_smem(Dv), stream);
+    } else if (mma) {
+        rc = mma_forward(a, dtype, stream);
+    } else {
+        rc = launch_attn(fn, a, dim3(p.tiles, N * Mk, a.splits), dcnb::kAttnThreads,
+                         dcnb::attn_fwd_smem(p.bq, D, ct), stream);
+    }
     if (rc != DCN_OK || a.splits == 1) return rc;
     return launch_attn(join, a, dim3((unsigned)((rows_total + 7) / 8)), 256, 0, stream);
 }
