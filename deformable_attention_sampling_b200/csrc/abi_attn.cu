@@ -474,7 +474,7 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
                          dcnb::attn_fwd_smem(p.bq, D, ct), stream);
     }
     if (rc != DCN_OK || a.splits == 1) return rc;
-    return launch_attn(join, a, dim3((unsigned)((rows_total + 7) / 8)), 256, 0, stream);
+    return launch_attn(join, a, dim3((unsigned)rows_total), dcnb::kJoinThreads, 0, stream);
 }
 
 long long diff_attn_backward_workspace_size(int N, int Lq, int Lk, int M, int Mk, int D, int Dv,
@@ -571,6 +571,8 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
     d.rowv = ws;
     d.scales = ws + rowv_floats(N, Lq, M);
     d.glam = grad_lambda;
+    d.vec4 = Dv % 4 == 0 &&
+             ((uintptr_t)out | (uintptr_t)out2 | (uintptr_t)grad_out) % (uintptr_t)(4 * es) == 0;
     const long long g_blocks = rowv_floats(N, Lq, M) / (4 * 8);
     const long long v_blocks = mma && dtype == DCN_F16 ? (keys * Mk + 7) / 8 : 0;
     if (g_blocks + v_blocks > kInt31) return DCN_ERR_UNSUPPORTED;

@@ -7,7 +7,7 @@ using namespace dcnb_abi;
 
 namespace {
 
-constexpr int kNormBlockThreads = 256;
+constexpr int kNormBlockThreads = dcnb::kNormSmall;
 
 struct NormShape {
     int es;
@@ -27,12 +27,12 @@ NormShape norm_shape(int es, long long rows, int C) {
     return s;
 }
 
-// Blocks that share an image's rows in the gradient: about three blocks a
-// multiprocessor over all images (more only adds partial rows to sum), at
+// Blocks that share an image's rows in the gradient: two blocks a
+// multiprocessor (its registers hold no more) over all images (more only adds partial rows to sum), at
 // least one team step each.
 int grad_blocks_per_image(long long images, long long rows_per_image, int teams, int threads) {
-    const long long wanted = 3LL * sm_count() * kNormBlockThreads / threads;
-    long long per = (wanted + images - 1) / images;
+    const long long wanted = std::max(2LL * sm_count() * kNormBlockThreads / threads, 1LL);
+    long long per = wanted / images;
     per = std::min(per, (rows_per_image + teams - 1) / teams);
     return (int)std::max(per, 1LL);
 }
@@ -61,20 +61,29 @@ bool clash(const Span& a, const Span& b) {
     return a.p && b.p && a.bytes > 0 && b.bytes > 0 && overlaps(a.p, a.bytes, b.p, b.bytes);
 }
 
-template <typename T>
-const void* norm_kernel_for(bool vec, bool grad) {
-    if (grad)
-        return vec ? (const void*)dcnb::norm_residual_grad_kernel<T, true>
-                   : (const void*)dcnb::norm_residual_grad_kernel<T, false>;
-    return vec ? (const void*)dcnb::norm_residual_kernel<T, true>
-               : (const void*)dcnb::norm_residual_kernel<T, false>;
+template <typename T, bool VEC>
+const void* norm_kernel_threads(int threads, bool grad) {
+    if (threads <= dcnb::kNormSmall)
+        return grad ? (const void*)dcnb::norm_residual_grad_kernel<T, VEC, dcnb::kNormSmall>
+                    : (const void*)dcnb::norm_residual_kernel<T, VEC, dcnb::kNormSmall>;
+    if (threads <= dcnb::kNormMiddle)
+        return grad ? (const void*)dcnb::norm_residual_grad_kernel<T, VEC, dcnb::kNormMiddle>
+                    : (const void*)dcnb::norm_residual_kernel<T, VEC, dcnb::kNormMiddle>;
+    return grad ? (const void*)dcnb::norm_residual_grad_kernel<T, VEC, dcnb::kNormMaxThreads>
+                : (const void*)dcnb::norm_residual_kernel<T, VEC, dcnb::kNormMaxThreads>;
 }
 
-const void* norm_kernel(int dtype, bool vec, bool grad) {
+template <typename T>
+const void* norm_kernel_for(bool vec, int threads, bool grad) {
+    return vec ? norm_kernel_threads<T, true>(threads, grad)
+               : norm_kernel_threads<T, false>(threads, grad);
+}
+
+const void* norm_kernel(int dtype, bool vec, int threads, bool grad) {
     switch (dtype) {
-        case DCN_F32: return norm_kernel_for<float>(vec, grad);
-        case DCN_F16: return norm_kernel_for<__half>(vec, grad);
-        case DCN_BF16: return norm_kernel_for<__nv_bfloat16>(vec, grad);
+        case DCN_F32: return norm_kernel_for<float>(vec, threads, grad);
+        case DCN_F16: return norm_kernel_for<__half>(vec, threads, grad);
+        case DCN_BF16: return norm_kernel_for<__nv_bfloat16>(vec, threads, grad);
         default: return nullptr;
     }
 }
@@ -138,7 +147,7 @@ int norm_residual_forward(const void* x, const void* y, const void* scale, const
     a.pre = pre;
     a.eps = eps;
     const bool vec = C % dcnb::kNormV == 0 && bits % 16 == 0;
-    const void* fn = norm_kernel(dtype, vec, false);
+    const void* fn = norm_kernel(dtype, vec, s.threads, false);
     const long long blocks = (rows + s.teams - 1) / s.teams;
     return launch(fn, a, (int)std::min(blocks, kInt31), s.threads, 0, stream);
 }
@@ -221,7 +230,7 @@ int norm_residual_backward(const void* y, const void* z, const void* grad_z, con
         a.pre = pre;
         a.eps = eps;
         const bool vec = C % dcnb::kNormV == 0 && row_bits % 16 == 0;
-        const void* fn = norm_kernel(dtype, vec, true);
+        const void* fn = norm_kernel(dtype, vec, s.threads, true);
         const int smem = (s.teams - 1) * s.tpr * dcnb::kNormV * 4;
         const int rc = launch_grid(fn, a, (int)(a.images * a.blocks_per_image), s.threads, smem,
                                    stream);

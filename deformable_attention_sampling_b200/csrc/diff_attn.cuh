@@ -366,60 +366,65 @@ __global__ void __launch_bounds__(kAttnThreads) diff_attn_kernel(const AttnArgs 
     }
 }
 
-// Joins the splits of a row: O_s and l_s weighted by 2^(m_s - max).  One warp
-// per row.
+// Joins the splits of a row: O_s and l_s weighted by 2^(m_s - max), in the order
+// of the splits.  One block per row: a warp a map forms the weights, then every
+// thread sums its columns (loads of a warp are whole rows, and independent of
+// one another).
+constexpr int kJoinThreads = 128;
+
 template <typename T>
-__global__ void __launch_bounds__(256) diff_attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) diff_attn_join_kernel(const AttnArgs a) {
+    __shared__ float weight[2][kAttnMaxSplits], inv[2];
     const long long total = (long long)a.N * a.Mk * a.rows;
-    const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (at >= total) return;
+    const long long at = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nk = (int)(at / a.rows), row = (int)(at - (long long)nk * a.rows);
     const int n = (int)a.div_Mk.div((uint32_t)nk), kv = nk - n * a.Mk;
     const uint32_t tok = a.div_G.div((uint32_t)row);
     const int head = kv * a.G + row - (int)tok * a.G, Dv = a.Dv;
-    float w[2][2], inv[2], lse[2];        // lane holds splits lane and lane + 32
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        float m[2], l[2];
+    if (warp < 2) {
+        float m[2], l[2];                 // lane holds splits lane and lane + 32
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int sp = lane + 32 * h;
-            const long long p = (((long long)sp * total + at) * 2 + s) * 2;
+            const long long p = (((long long)sp * total + at) * 2 + warp) * 2;
             m[h] = sp < a.splits ? a.part_ml[p] : -INFINITY;
             l[h] = sp < a.splits ? a.part_ml[p + 1] : 0.f;
         }
         float top = fmaxf(m[0], m[1]);
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float base = top == -INFINITY ? 0.f : top;
-        w[s][0] = exp2f(m[0] - base);
-        w[s][1] = exp2f(m[1] - base);
-        float sum = w[s][0] * l[0] + w[s][1] * l[1];
+        float w[2], sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w[h] = exp2f(m[h] - base);
+            sum += w[h] * l[h];
+            if (lane + 32 * h < kAttnMaxSplits) weight[warp][lane + 32 * h] = w[h];
+        }
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        inv[s] = sum > 0.f ? 1.f / sum : 0.f;
-        lse[s] = sum > 0.f ? base + log2f(sum) : INFINITY;
+        if (lane == 0) {
+            inv[warp] = sum > 0.f ? 1.f / sum : 0.f;
+            if (a.lse)
+                a.lse[(((long long)n * a.M + head) * 2 + warp) * a.Lq + tok] =
+                    sum > 0.f ? base + log2f(sum) : INFINITY;
+        }
     }
+    __syncthreads();
     const float lam = Elem<T>::one(static_cast<const T*>(a.lam) + head);
     const long long to = (((long long)n * a.Lq + tok) * a.M + head) * Dv;
-    for (int c0 = 0; c0 < Dv; c0 += 32) {       // every lane takes part in the shuffles
-        const int c = c0 + lane;
-        float o[2] = {0.f, 0.f};
-        for (int sp = 0; sp < a.splits; ++sp) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const float ws = __shfl_sync(0xffffffffu, sp < 32 ? w[s][0] : w[s][1], sp & 31);
-                if (c < Dv && ws > 0.f)
-                    o[s] += ws * a.part_o[(((long long)sp * total + at) * 2 + s) * Dv + c];
-            }
+    const long long step = total * 2 * Dv;
+    for (int c = threadIdx.x; c < Dv; c += kJoinThreads) {
+        const float* p = a.part_o + at * 2 * Dv + c;
+        float x = 0.f, y = 0.f;
+#pragma unroll 8
+        for (int sp = 0; sp < a.splits; ++sp, p += step) {
+            x = fmaf(weight[0][sp], p[0], x);
+            y = fmaf(weight[1][sp], p[Dv], y);
         }
-        if (c < Dv) {
-            const float second = o[1] * inv[1];
-            static_cast<T*>(a.out)[to + c] = Elem<T>::from(o[0] * inv[0] - lam * second);
-            if (a.out2) static_cast<T*>(a.out2)[to + c] = Elem<T>::from(second);
-        }
+        y *= inv[1];
+        static_cast<T*>(a.out)[to + c] = Elem<T>::from(x * inv[0] - lam * y);
+        if (a.out2) static_cast<T*>(a.out2)[to + c] = Elem<T>::from(y);
     }
-    if (a.lse && lane < 2)
-        a.lse[(((long long)n * a.M + head) * 2 + lane) * a.Lq + tok] = lane ? lse[1] : lse[0];
 }
 
 // ---------------------------------------------------------------- gradient --
@@ -446,6 +451,7 @@ struct AttnDeltaArgs {
     float* peak;           // [blocks] largest |g|^2 and |v|^2 of a block, or null
     float* scales;         // cs, cp
     int g_blocks, v_blocks;
+    int vec4;              // rows of out, out2 and grad_out are aligned groups of 4
 };
 
 // One warp per (token, head), tokens padded to whole tiles: e_1 = <g, O_1> from
@@ -473,11 +479,14 @@ __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArg
                 const T* g = static_cast<const T*>(d.go) + row;
                 const T* o = static_cast<const T*>(d.out) + row;
                 const T* o2 = static_cast<const T*>(d.out2) + row;
-                for (int c = lane; c < a.Dv; c += 32) {
-                    const float gv = Elem<T>::one(g + c);
-                    s = fmaf(gv, Elem<T>::one(o + c), s);
-                    s2 = fmaf(gv, Elem<T>::one(o2 + c), s2);
-                    peak = fmaf(gv, gv, peak);
+                // four channels a lane where rows are aligned groups of four
+                for (int c = 4 * lane; c < a.Dv; c += 128) {
+                    const float4 gv = attn_ld4<T>(g, c, a.Dv, d.vec4);
+                    const float4 ov = attn_ld4<T>(o, c, a.Dv, d.vec4);
+                    const float4 o2v = attn_ld4<T>(o2, c, a.Dv, d.vec4);
+                    s = dot4(s, gv, ov);
+                    s2 = dot4(s2, gv, o2v);
+                    peak = dot4(peak, gv, gv);
                 }
                 if (lane < 2) lse = d.lse[(((long long)n * a.M + h) * 2 + lane) * a.Lq + i];
             }

@@ -62,6 +62,32 @@ struct NormArgs {
     float eps;
 };
 
+// Eight channels of a row as stored, loaded ahead of their use.
+template <typename T>
+struct NormRaw {
+    uint32_t w[2 * sizeof(T)];
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void norm_fetch(const void* p, long long at, int c, int C, bool live,
+                                           NormRaw<T>& r) {
+    const T* q = static_cast<const T*>(p) + at + c;
+    if constexpr (VEC) {
+        if (live && c < C) {
+            ld_words<16>(q, r.w);
+            if constexpr (sizeof(T) == 4) ld_words<16>(q + 4, r.w + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * (int)sizeof(T); ++i) r.w[i] = 0u;
+        }
+    } else {
+        float f[kNormV];               // widening and rounding back are exact
+#pragma unroll
+        for (int e = 0; e < kNormV; ++e) f[e] = live && c + e < C ? Elem<T>::one(q + e) : 0.f;
+        narrow<T, kNormV>(f, r.w);
+    }
+}
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void norm_load(const void* p, long long at, int c, int C, float* f) {
     const T* q = static_cast<const T*>(p) + at;
@@ -147,8 +173,17 @@ struct TeamSum {
     }
 };
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(1024) norm_residual_kernel(const NormArgs a) {
+// Blocks of 256 threads (rows of up to 2048 channels) and of 512 (up to 4096)
+// have 128 registers a thread, which hold every factor and the next row; longer
+// rows take 1024 threads at 64.
+constexpr int kNormSmall = 256;
+constexpr int kNormMiddle = 512;
+
+// A team works on two rows at a time: one sum over the team serves both, and
+// four tensors' loads are in flight beside the next two rows'.
+template <typename T, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == kNormSmall ? 2 : 1)
+    norm_residual_kernel(const NormArgs a) {
     __shared__ float2 buf[64];
     const int tpr = a.tpr, teams = blockDim.x / tpr;
     const int team = threadIdx.x / tpr, c = (threadIdx.x & (tpr - 1)) * kNormV, C = a.C;
@@ -157,76 +192,82 @@ __global__ void __launch_bounds__(1024) norm_residual_kernel(const NormArgs a) {
     const long long r_begin = rows * blockIdx.x / gridDim.x;
     const long long r_end = rows * (blockIdx.x + 1) / gridDim.x;
     const float inv_c = 1.f / (float)C;
-    float pw[kNormV], pb[kNormV], sc[kNormV], qw[kNormV], qb[kNormV], gt[kNormV];
+    float pw[kNormV], pb[kNormV], sc[kNormV], qw[kNormV], qb[kNormV];
     norm_factor<T, VEC>(a.post_w, 0, c, C, 1.f, pw);
     norm_factor<T, VEC>(a.post_b, 0, c, C, 0.f, pb);
     norm_factor<T, VEC>(a.scale, 0, c, C, 1.f, sc);
     norm_factor<T, VEC>(a.pre_w, 0, c, C, 1.f, qw);
     norm_factor<T, VEC>(a.pre_b, 0, c, C, 0.f, qb);
-    long long image = -1;
-    // all teams of a block take the same number of steps (barriers in the sums)
-    for (long long r0 = r_begin; r0 < r_end; r0 += teams) {
-        const long long r = r0 + team;
-        const bool live = r < r_end;
-        float xv[kNormV], u[kNormV];
-        if (live) {
-            norm_load<T, VEC>(a.y, r * C, c, C, u);
-            norm_load<T, VEC>(a.x, r * C, c, C, xv);
-            if (a.gate) {
-                const long long n = r / a.rows_per_image;
-                if (n != image) {
-                    norm_load<T, VEC>(a.gate, n * C, c, C, gt);
-                    image = n;
-                }
-            }
-        } else {
+    // The normalised rows in place of v, from both rows' sums over the team.
+    auto normalise = [&](float (&v)[2][kNormV]) {
+        if (!a.rms) {
+            float s[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < kNormV; ++e) u[e] = xv[e] = 0.f;
-        }
-        if (a.post) {
-            float mean = 0.f;
-            if (!a.rms) {
-                float s = 0.f;
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int e = 0; e < kNormV; ++e) s += u[e];
-                mean = sum(s, 0.f).x * inv_c;
-            }
-            float q = 0.f;
+                for (int e = 0; e < kNormV; ++e) s[k] += v[k][e];
+            const float2 m = sum(s[0], s[1]);
 #pragma unroll
             for (int e = 0; e < kNormV; ++e) {
-                u[e] = c + e < C ? u[e] - mean : 0.f;
-                q += u[e] * u[e];
+                v[0][e] = c + e < C ? v[0][e] - m.x * inv_c : 0.f;
+                v[1][e] = c + e < C ? v[1][e] - m.y * inv_c : 0.f;
             }
-            const float rs = 1.0f / sqrtf(sum(q, 0.f).x * inv_c + a.eps);
-#pragma unroll
-            for (int e = 0; e < kNormV; ++e) u[e] = u[e] * rs * pw[e] + pb[e];
         }
-        float z[kNormV];
+        float q[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < kNormV; ++e) q[k] += v[k][e] * v[k][e];
+        const float2 t = sum(q[0], q[1]);
+        const float r0 = 1.0f / sqrtf(t.x * inv_c + a.eps), r1 = 1.0f / sqrtf(t.y * inv_c + a.eps);
 #pragma unroll
         for (int e = 0; e < kNormV; ++e) {
-            const float f = a.gate ? sc[e] * gt[e] : sc[e];
-            z[e] = c + e < C ? xv[e] + f * u[e] : 0.f;
+            v[0][e] *= r0;
+            v[1][e] *= r1;
         }
-        if (live) norm_store<T, VEC>(a.z, r * C, c, C, z);
-        if (a.pre) {
-            float mean = 0.f;
-            if (!a.rms) {
-                float s = 0.f;
+    };
+    NormRaw<T> ry[2], rx[2];
+    auto fetch = [&](long long r) {
 #pragma unroll
-                for (int e = 0; e < kNormV; ++e) s += z[e];
-                mean = sum(s, 0.f).x * inv_c;
-            }
-            float q = 0.f;
+        for (int k = 0; k < 2; ++k) {
+            const long long at = r + k * teams;
+            norm_fetch<T, VEC>(a.y, at * C, c, C, at < r_end, ry[k]);
+            norm_fetch<T, VEC>(a.x, at * C, c, C, at < r_end, rx[k]);
+        }
+    };
+    fetch(r_begin + team);
+    // all teams of a block take the same number of steps (barriers in the sums)
+    for (long long r0 = r_begin; r0 < r_end; r0 += 2 * teams) {
+        float z[2][kNormV], v[2][kNormV];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            widen<T, kNormV>(rx[k].w, z[k]);
+            widen<T, kNormV>(ry[k].w, v[k]);
+        }
+        fetch(r0 + team + 2 * teams);
+        if (a.post) normalise(v);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const long long r = r0 + team + k * teams;
+            const bool live = r < r_end;
+            float gt[kNormV];
+            norm_factor<T, VEC>(live ? a.gate : nullptr, live ? r / a.rows_per_image * C : 0, c, C,
+                                1.f, gt);
 #pragma unroll
             for (int e = 0; e < kNormV; ++e) {
-                z[e] = c + e < C ? z[e] - mean : 0.f;
-                q += z[e] * z[e];
+                const float u = a.post ? v[k][e] * pw[e] + pb[e] : v[k][e];
+                z[k][e] = c + e < C ? z[k][e] + sc[e] * gt[e] * u : 0.f;
             }
-            const float rs = 1.0f / sqrtf(sum(q, 0.f).x * inv_c + a.eps);
-            if (live) {
+            if (live) norm_store<T, VEC>(a.z, r * C, c, C, z[k]);
+        }
+        if (a.pre) {
+            normalise(z);
 #pragma unroll
-                for (int e = 0; e < kNormV; ++e) z[e] = z[e] * rs * qw[e] + qb[e];
-                norm_store<T, VEC>(a.h, r * C, c, C, z);
+            for (int k = 0; k < 2; ++k) {
+                const long long r = r0 + team + k * teams;
+#pragma unroll
+                for (int e = 0; e < kNormV; ++e) z[k][e] = z[k][e] * qw[e] + qb[e];
+                if (r < r_end) norm_store<T, VEC>(a.h, r * C, c, C, z[k]);
             }
         }
     }
@@ -234,8 +275,9 @@ __global__ void __launch_bounds__(1024) norm_residual_kernel(const NormArgs a) {
 
 // Rows' gradients and the blocks' column sums.  Block b sums rows of image
 // b / blocks_per_image only.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(1024) norm_residual_grad_kernel(const NormArgs a) {
+template <typename T, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == kNormSmall ? 2 : 1)
+    norm_residual_grad_kernel(const NormArgs a) {
     __shared__ float2 buf[64];
     extern __shared__ float norm_cols[];       // [teams - 1][tpr * 8] of one sum
     const int tpr = a.tpr, teams = blockDim.x / tpr;
@@ -261,23 +303,24 @@ __global__ void __launch_bounds__(1024) norm_residual_grad_kernel(const NormArgs
             sA[e] = sB[e] = sE[e] = sF[e] = 0.f;
         }
     }
+    NormRaw<T> ry, rz, rg, rh;
+    auto fetch = [&](long long r) {
+        const bool live = r < r_end;
+        norm_fetch<T, VEC>(a.y, r * C, c, C, live, ry);
+        norm_fetch<T, VEC>(a.gz, r * C, c, C, live, rg);
+        norm_fetch<T, VEC>(a.z, r * C, c, C, live && a.pre, rz);
+        norm_fetch<T, VEC>(a.gh, r * C, c, C, live && a.pre, rh);
+    };
+    fetch(r_begin + team);
     for (long long r0 = r_begin; r0 < r_end; r0 += teams) {
         const long long r = r0 + team;
         const bool live = r < r_end;
         float yv[kNormV], zv[kNormV], g[kNormV], gh[kNormV];
-        if (live) {
-            norm_load<T, VEC>(a.y, r * C, c, C, yv);
-            norm_load<T, VEC>(a.gz, r * C, c, C, g);
-            if (a.pre) {
-                norm_load<T, VEC>(a.z, r * C, c, C, zv);
-                norm_load<T, VEC>(a.gh, r * C, c, C, gh);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < kNormV; ++e) {
-            if (!live) yv[e] = g[e] = 0.f;
-            if (!live || !a.pre) zv[e] = gh[e] = 0.f;
-        }
+        widen<T, kNormV>(ry.w, yv);
+        widen<T, kNormV>(rz.w, zv);
+        widen<T, kNormV>(rg.w, g);
+        widen<T, kNormV>(rh.w, gh);
+        fetch(r + teams);
         // both norms' statistics, two sums at a time
         float my = 0.f, mz = 0.f, r1 = 0.f, r2 = 0.f;
         if (!a.rms) {
