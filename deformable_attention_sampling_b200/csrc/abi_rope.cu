@@ -98,14 +98,18 @@ int rope_launch(const void* x, const float* pos, const float* freqs, const void*
     a.images = grad_pos && pos_images == 1 ? N : 1;
     a.units = a.images > 1 ? L : (long long)N * L;
     a.tasks = (interleaved && v > 1) ? D / v : (int)(R / v + (D - 2 * R) / v);
-    a.total_tasks = M * a.tasks;
     // lanes per token: about two tasks a lane, at most a warp
+    const long long total = (long long)M * a.tasks;
     int tpt = 1;
-    while (tpt < 32 && 2 * tpt < a.total_tasks) tpt <<= 1;
+    while (tpt < 32 && 2 * tpt < total) tpt <<= 1;
+    // a team writes its token's A position gradients from as many lanes
+    while (tpt < A) tpt <<= 1;
     // a team's turns live in shared memory: at most 48 KB a block
     while (tpt < 32 && (dcnb::kRopeThreads / tpt) * R * 8 > kMaxStageBytes) tpt <<= 1;
     a.tpt = tpt;
-    a.div_tasks = make_div((uint32_t)a.tasks);
+    a.jl = std::min(a.tasks, tpt);
+    a.hl = tpt / a.jl;
+    a.div_jl = make_div((uint32_t)a.jl);
     a.div_L = make_div((uint32_t)L);
     a.sign = inverse ? -1.f : 1.f;
 

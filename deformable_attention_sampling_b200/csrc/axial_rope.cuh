@@ -41,8 +41,8 @@ struct RopeArgs {
     int shared_pos;            // 1: pos has one image for all
     int tpt;                   // lanes per token, a power of two
     int tasks;                 // vector tasks per head
-    int total_tasks;           // M * tasks
-    FastDiv div_tasks, div_L;
+    int jl, hl;                // a team's lanes over a head's tasks, heads side by side
+    FastDiv div_jl, div_L;
     float sign;                // -1: turn backwards
 };
 
@@ -88,9 +88,17 @@ __device__ __forceinline__ void st_f32(T* p, const float* f) {
 // V elements per access.  INTER with V > 1: a task is one vector of V channels
 // (V / 2 pairs, or V channels that pass).  Halves, or V = 1: a task is V pairs
 // in two vectors, or one vector that passes.
+// A team's lanes lie side by side over a head's tasks (jl of them) and over
+// heads: a lane keeps its task, its turns in registers and the sums of its
+// pairs' position gradients, and steps over the heads with the next one's loads
+// in flight.
 template <typename T, int V, bool INTER, bool GRAD>
 __global__ void __launch_bounds__(kRopeThreads) axial_rope_kernel(const RopeArgs a) {
     extern __shared__ float2 rope_turns[];       // [teams][R] (cos, sin)
+    constexpr bool VINTER = INTER && V > 1;
+    constexpr int P = VINTER ? V / 2 : V;        // pairs of a task
+    constexpr int NV = VINTER ? 1 : 2;           // vectors of a task
+    constexpr int W = (V * (int)sizeof(T) + 3) / 4;
     const int tpt = a.tpt;
     const int team = threadIdx.x / tpt, lane = threadIdx.x & (tpt - 1);
     const long long unit = (long long)blockIdx.x * (kRopeThreads / tpt) + team;
@@ -100,6 +108,35 @@ __global__ void __launch_bounds__(kRopeThreads) axial_rope_kernel(const RopeArgs
     const uint32_t img = a.images > 1 ? 0u : a.div_L.div(u);
     const uint32_t l = a.images > 1 ? u : u - img * (uint32_t)a.L;
     const long long prow = a.shared_pos ? (long long)l : (long long)img * a.L + l;
+    const int hsub = (int)a.div_jl.div((uint32_t)lane);
+    const int j0 = lane - hsub * a.jl;
+    const bool want_pos = GRAD && a.grad_pos != nullptr;
+
+    uint32_t src_w[NV][W], x_w[NV][W];           // the next head's vectors
+    // first channel of each vector of task j
+    auto channel = [&](int j, int v) {
+        if (VINTER) return j * V;
+        const int i0 = j * V;
+        if (i0 >= a.R) return i0 + a.R;          // 2R + (i0 - R): passes, one vector
+        return INTER ? 2 * i0 + v : i0 + v * a.R;
+    };
+    auto fetch = [&](int n, int j, int m) {
+        if (m >= a.M) return;
+        const long long token = ((long long)img + n) * a.L + l;
+        const T* x = static_cast<const T*>(a.x) + ((long long)img + n) * a.x_image +
+                     (long long)l * a.x_row + m * a.D;
+        const T* src = GRAD ? static_cast<const T*>(a.go) + token * ((long long)a.M * a.D) + m * a.D
+                            : x;
+        const bool turned = VINTER ? j * V < 2 * a.R : j * V < a.R;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if (v == 1 && !turned) break;
+            ld_words<V * (int)sizeof(T)>(src + channel(j, v), src_w[v]);
+            if (want_pos && turned) ld_words<V * (int)sizeof(T)>(x + channel(j, v), x_w[v]);
+        }
+    };
+    const bool active = live && hsub < a.hl;
+    if (active && j0 < a.tasks) fetch(0, j0, hsub);
     if (live) {
         for (int i = lane; i < a.R; i += tpt) {
             int ax = 0;
@@ -114,87 +151,61 @@ __global__ void __launch_bounds__(kRopeThreads) axial_rope_kernel(const RopeArgs
     }
     __syncwarp();
     float acc[kRopeMaxAxes] = {0.f, 0.f, 0.f, 0.f};
-    constexpr bool VINTER = INTER && V > 1;
-    const bool want_pos = GRAD && a.grad_pos != nullptr;
-    if (live) {
-        for (int n = 0; n < a.images; ++n) {
-            const long long token = ((long long)img + n) * a.L + l;
-            const T* x = static_cast<const T*>(a.x) + ((long long)img + n) * a.x_image +
-                         (long long)l * a.x_row;
-            const long long base = token * ((long long)a.M * a.D);
-            const T* src = GRAD ? static_cast<const T*>(a.go) + base : x;
-            T* out = static_cast<T*>(a.out) + base;
-#pragma unroll 2
-            for (int t = lane; t < a.total_tasks; t += tpt) {
-                const int m = (int)a.div_tasks.div((uint32_t)t);
-                const int j = t - m * a.tasks;
-                const int head = m * a.D;
-                if constexpr (VINTER) {
-                    const int c = j * V;
-                    float f[V], r[V];
-                    ld_f32<T, V>(src + head + c, f);
-                    if (c < 2 * a.R) {
-                        float xv[V];
-                        if (want_pos) ld_f32<T, V>(x + head + c, xv);
+    if (active) {
+        for (int j = j0; j < a.tasks; j += a.jl) {
+            const bool turned = VINTER ? j * V < 2 * a.R : j * V < a.R;
+            float2 cs[P];
+            float sums[P];
 #pragma unroll
-                        for (int e = 0; e < V; e += 2) {
-                            const int i = (c + e) >> 1;
-                            const float2 cs = turns[i];
+            for (int e = 0; e < P; ++e) {
+                cs[e] = turned ? turns[j * P + e] : make_float2(1.f, 0.f);
+                sums[e] = 0.f;
+            }
+            for (int n = 0; n < a.images; ++n) {
+                if (j != j0 || n > 0) fetch(n, j, hsub);
+                T* out = static_cast<T*>(a.out) +
+                         (((long long)img + n) * a.L + l) * ((long long)a.M * a.D);
+                for (int m = hsub; m < a.M; m += a.hl) {
+                    float f[NV][V], xv[NV][V];
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        widen<T, V>(src_w[v], f[v]);
+                        if (want_pos) widen<T, V>(x_w[v], xv[v]);
+                    }
+                    fetch(n, j, m + a.hl);
+                    if (turned) {
+#pragma unroll
+                        for (int e = 0; e < P; ++e) {
+                            float& fa = VINTER ? f[0][2 * e] : f[0][e];
+                            float& fb = VINTER ? f[0][2 * e + 1] : f[NV - 1][e];
                             // GRAD: the turn by -th of the gradient
-                            const float s = GRAD ? -cs.y : cs.y;
-                            r[e] = f[e] * cs.x - f[e + 1] * s;
-                            r[e + 1] = f[e] * s + f[e + 1] * cs.x;
+                            const float s = GRAD ? -cs[e].y : cs[e].y;
                             if (want_pos) {
-                                const float oa = xv[e] * cs.x - xv[e + 1] * cs.y;
-                                const float ob = xv[e] * cs.y + xv[e + 1] * cs.x;
-                                const float d = a.freqs[i] * (f[e + 1] * oa - f[e] * ob);
-                                int ax = 0;
-                                while (ax + 1 < a.A && i >= a.pair_end[ax]) ++ax;
-#pragma unroll
-                                for (int k = 0; k < kRopeMaxAxes; ++k) acc[k] += k == ax ? d : 0.f;
+                                const float xa = VINTER ? xv[0][2 * e] : xv[0][e];
+                                const float xb = VINTER ? xv[0][2 * e + 1] : xv[NV - 1][e];
+                                const float oa = xa * cs[e].x - xb * cs[e].y;
+                                const float ob = xa * cs[e].y + xb * cs[e].x;
+                                sums[e] += fb * oa - fa * ob;
                             }
+                            const float ra = fa * cs[e].x - fb * s;
+                            fb = fa * s + fb * cs[e].x;
+                            fa = ra;
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < V; ++e) r[e] = f[e];
                     }
-                    st_f32<T, V>(out + head + c, r);
-                } else {
-                    const int i0 = j * V;
-                    if (i0 < a.R) {
-                        const int ca = head + (INTER ? 2 * i0 : i0);
-                        const int cb = head + (INTER ? 2 * i0 + 1 : i0 + a.R);
-                        float fa[V], fb[V], xa[V], xb[V], ra[V], rb[V];
-                        ld_f32<T, V>(src + ca, fa);
-                        ld_f32<T, V>(src + cb, fb);
-                        if (want_pos) {
-                            ld_f32<T, V>(x + ca, xa);
-                            ld_f32<T, V>(x + cb, xb);
-                        }
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            const float2 cs = turns[i0 + e];
-                            const float s = GRAD ? -cs.y : cs.y;
-                            ra[e] = fa[e] * cs.x - fb[e] * s;
-                            rb[e] = fa[e] * s + fb[e] * cs.x;
-                            if (want_pos) {
-                                const float oa = xa[e] * cs.x - xb[e] * cs.y;
-                                const float ob = xa[e] * cs.y + xb[e] * cs.x;
-                                const float d = a.freqs[i0 + e] * (fb[e] * oa - fa[e] * ob);
-                                int ax = 0;
-                                while (ax + 1 < a.A && i0 + e >= a.pair_end[ax]) ++ax;
+                    for (int v = 0; v < NV; ++v)
+                        if (v == 0 || turned) st_f32<T, V>(out + m * a.D + channel(j, v), f[v]);
+                }
+            }
+            if (want_pos && turned) {
 #pragma unroll
-                                for (int k = 0; k < kRopeMaxAxes; ++k) acc[k] += k == ax ? d : 0.f;
-                            }
-                        }
-                        st_f32<T, V>(out + ca, ra);
-                        st_f32<T, V>(out + cb, rb);
-                    } else {
-                        const int c = head + i0 + a.R;      // 2R + (i0 - R)
-                        float f[V];
-                        ld_f32<T, V>(src + c, f);
-                        st_f32<T, V>(out + c, f);
-                    }
+                for (int e = 0; e < P; ++e) {
+                    const int i = j * P + e;
+                    int ax = 0;
+                    while (ax + 1 < a.A && i >= a.pair_end[ax]) ++ax;
+                    const float d = a.freqs[i] * sums[e];
+#pragma unroll
+                    for (int k = 0; k < kRopeMaxAxes; ++k) acc[k] += k == ax ? d : 0.f;
                 }
             }
         }
