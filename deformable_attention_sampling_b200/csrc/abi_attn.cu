@@ -264,11 +264,11 @@ bool step_sizes(int dtype, int D, int Dv) {
 }
 
 // Key splits of the few-token kernel: 3 CTAs of 4 warps a multiprocessor run, and
-// about three rounds of them even out images of different lengths; a split has
-// at least 256 keys.
+// three full rounds of them even out images of different lengths (a fourth,
+// nearly empty one would not); a split has at least 256 keys.
 int step_splits(int N, int Lq, int Lk, int M, int Mk) {
     const long long ctas = (long long)ceil_div(Lq * (M / Mk), dcnb::kAsRows) * N * Mk;
-    long long s = (9LL * sm_count() + ctas - 1) / std::max(ctas, 1LL);
+    long long s = 9LL * sm_count() / std::max(ctas, 1LL);
     s = std::min(s, (long long)ceil_div(Lk, 256));
     return (int)std::max(1LL, std::min(s, (long long)dcnb::kAttnMaxSplits));
 }
@@ -466,7 +466,7 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
     if (step) {
         fn = dtype == DCN_BF16 ? step_kernel<__nv_bfloat16>(D, Dv) : step_kernel<__half>(D, Dv);
         rc = launch_attn(fn, a, dim3(ceil_div(a.rows, dcnb::kAsRows), N * Mk, a.splits),
-                         dcnb::kAsThreads, dcnb::attn_step_smem(Dv), stream);
+                         dcnb::kAsThreads, dcnb::attn_step_smem(D, Dv), stream);
     } else if (mma) {
         rc = mma_forward(a, dtype, stream);
     } else {

@@ -3,7 +3,7 @@
 //
 // Bound: the key and value bytes.  So every key and value is read once, from
 // global memory straight into the registers of matrix instructions
-// (mma.sync m16n8k16; tcgen05's 128 rows would be empty), and nothing is staged.
+// (mma.sync m16n8k16; tcgen05's 128 rows would be empty), and no lane reads what another loaded.
 // A warp owns 8 packed rows (the tokens and heads that share a key / value
 // head) and walks blocks of 16 keys.  The two maps sit in one 16-row tile:
 //   scores   rows 0-7 = Q_0 K_0^T, rows 8-15 = Q_1 K_1^T: map 0's product has
@@ -11,10 +11,12 @@
 //            both add into one accumulator;
 //   values   the 16 x 16 weights of both maps times one value block.
 // A contraction may run over its index in any order, so lane (g, t) = (lane / 4,
-// lane % 4) takes D / 4 consecutive channels of key g, whatever index the
-// instruction gives them, and Dv / 8 consecutive value channels of its four
-// keys, paired by byte permutes: all loads are 8 to 32 consecutive bytes a lane
-// and whole rows a group of lanes.
+// lane % 4) takes every fourth 16-byte piece of key g, whatever channels the
+// instruction means by them, and every eighth piece of its four keys' values,
+// paired by byte permutes: neighbouring lanes read neighbouring pieces, and no
+// sector is fetched twice.
+// A warp's next block is on its way to shared memory (cp.async, each lane its own
+// pieces, so no barrier) while it works on this one.
 // The keys are split over CTAs (and the 4 warps of a CTA, which join in shared
 // memory); diff_attn_join_kernel adds the CTAs' parts in a fixed order.
 #pragma once
@@ -47,31 +49,48 @@ __device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, ui
     }
 }
 
-// W words from p, in accesses of up to 16 bytes; zeros unless ok.
+// W words from p, 16-byte pieces 64 bytes apart; zeros unless ok.
 template <int W>
 __device__ __forceinline__ void ld_row_words(const void* p, bool ok, uint32_t* w) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0u;
     if (ok) {
-        if constexpr (W == 2) {
-            load_vec<8>(p, w);
-        } else {
 #pragma unroll
-            for (int i = 0; i < W; i += 4) load_vec<16>(static_cast<const char*>(p) + 4 * i, w + i);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = 0u;
+        for (int i = 0; i < W; i += 4) load_vec<16>(static_cast<const char*>(p) + 16 * i, w + i);
     }
 }
 
-__host__ __device__ constexpr int attn_step_smem(int Dv) {
-    return kAsWarps * 16 * (Dv + 2) * 4;
+// Asynchronous copy of VB bytes to shared memory; zeros unless ok.
+template <int VB>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok) {
+    const int n = ok ? VB : 0;
+    if constexpr (VB == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     :: "r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;"
+                     :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Bytes of a warp's block in shared memory: a lane's 16-byte pieces of two keys of
+// both maps and of four value rows.
+__host__ __device__ constexpr int attn_step_block(int D, int Dv) {
+    return (4 * (D / 32) + 4 * (Dv >= 64 ? Dv / 64 : 1)) * 512;
+}
+constexpr int kAsStages = 2;
+
+// The ring of the warps' blocks; the join of the warps takes its place afterwards.
+__host__ __device__ constexpr int attn_step_smem(int D, int Dv) {
+    const int ring = kAsWarps * kAsStages * attn_step_block(D, Dv);
+    const int join = kAsWarps * 16 * (Dv + 2) * 4;
+    return ring > join ? ring : join;
 }
 
 template <typename T, int D, int DV>
-__global__ void __launch_bounds__(kAsThreads, DV <= 64 && D <= 64 ? 4 : 3)
+__global__ void __launch_bounds__(kAsThreads, D == 128 && DV == 128 ? 2 : DV <= 64 && D <= 64 ? 4 : 3)
     diff_attn_step_kernel(const AttnArgs a) {
     constexpr float kBias = std::is_same<T, __half>::value ? 6.f : 0.f;
-    constexpr int KW = D / 8;              // words of a lane's channels of a key (D / 4 of them)
+    constexpr int KW = D / 8;              // words of a lane's channels of a key
     constexpr int CPG = DV / 8;            // value channels of a lane
     constexpr int VW = CPG / 2;
     constexpr int KS = D / 16;             // steps of 16 of the score product
@@ -96,35 +115,72 @@ __global__ void __launch_bounds__(kAsThreads, DV <= 64 && D <= 64 ? 4 : 3)
 #pragma unroll
     for (int m = 0; m < 2; ++m)
         ld_row_words<KW>(static_cast<const T*>(a.q) + n * a.q_image + (long long)tok * a.q_row +
-                             ((long long)head * 2 + m) * D + t * (D / 4),
+                             ((long long)head * 2 + m) * D + t * 8,
                          row < a.rows, q[m]);
-    const T* kb = static_cast<const T*>(a.k) + n * a.k_image + (long long)kv * 2 * D + t * (D / 4);
-    const T* vb = static_cast<const T*>(a.v) + n * a.v_image + (long long)kv * DV + g * CPG;
+    const T* kb = static_cast<const T*>(a.k) + n * a.k_image + (long long)kv * 2 * D + t * 8;
+    const T* vb = static_cast<const T*>(a.v) + n * a.v_image + (long long)kv * DV + g * (CPG < 8 ? CPG : 8);
     const unsigned char* mask = a.mask ? a.mask + (long long)n * a.Lk : nullptr;
 
     float o[CPG][4], top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < CPG; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     const float sc = a.scale_log2;
-    for (int b = b0 + warp; b < b1; b += kAsWarps) {
-        const int j0 = b * kAsKeys;
-        uint32_t kw[2][2][KW], vw[4][VW];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int key = j0 + 8 * h + g;
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-                ld_row_words<KW>(kb + (long long)key * a.k_row + m * D, key < len, kw[h][m]);
-        }
-        // keys 2t, 2t + 1, 2t + 8, 2t + 9: those whose weights the lane holds, too
+    constexpr int KP = KW / 4, VP = VW >= 4 ? VW / 4 : 1;      // 16-byte pieces
+    constexpr int VB = VW >= 4 ? 16 : 8;
+    const uint32_t ring = smem_u32(as_smem) +
+                          (uint32_t)(warp * kAsStages * attn_step_block(D, DV) + lane * 16);
+    // which of keys 2t, 2t + 1, 2t + 8, 2t + 9 some token may see
+    auto keys_seen = [&](int j0) {
         uint32_t seen = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int key = j0 + 2 * t + (u & 1) + 8 * (u >> 1);
-            const bool ok = key < len && !(mask && mask[key]);
-            ld_row_words<VW>(vb + (long long)key * a.v_row, ok, vw[u]);
-            seen |= (uint32_t)ok << u;
+            seen |= (uint32_t)(key < len && !(mask && mask[key])) << u;
         }
+        return seen;
+    };
+    auto fetch = [&](int b, int stage) {
+        if (b < b1) {
+            const int j0 = b * kAsKeys;
+            uint32_t dst = ring + (uint32_t)(stage * attn_step_block(D, DV));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = j0 + 8 * h + g;
+                const bool ok = key < len;
+                const T* p = kb + (long long)(ok ? key : j0) * a.k_row;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < KP; ++i, dst += 512)
+                        copy_async<16>(dst, p + m * D + 32 * i, ok);
+            }
+            const uint32_t seen = keys_seen(j0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool ok = seen >> u & 1;
+                const T* p = vb + (long long)(ok ? j0 + 2 * t + (u & 1) + 8 * (u >> 1) : j0) *
+                                      a.v_row;
+#pragma unroll
+                for (int i = 0; i < VP; ++i, dst += 512) copy_async<VB>(dst, p + 64 * i, ok);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(b0 + warp, 0);
+    int stage = 0;
+    for (int b = b0 + warp; b < b1; b += kAsWarps, stage ^= 1) {
+        const int j0 = b * kAsKeys;
+        fetch(b + kAsWarps, stage ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        uint32_t kw[2][2][KW], vw[4][VP * 4];
+        uint32_t src = ring + (uint32_t)(stage * attn_step_block(D, DV));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < KP; ++i, src += 512) lds128(src, kw[h][m] + 4 * i);
+        const uint32_t seen = keys_seen(j0);
         float s[2][4];                     // keys 2t, 2t + 1 (+ 8) of map 0's row, map 1's row
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -173,6 +229,10 @@ __global__ void __launch_bounds__(kAsThreads, DV <= 64 && D <= 64 ? 4 : 3)
         }
         const float ref[2] = {top[0] == -INFINITY ? 0.f : top[0],
                               top[1] == -INFINITY ? 0.f : top[1]};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < VP; ++i, src += 512) lds128(src, vw[u] + 4 * i);
         uint32_t p[2][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -195,6 +255,7 @@ __global__ void __launch_bounds__(kAsThreads, DV <= 64 && D <= 64 ? 4 : 3)
         sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], 1);
         sum[m] += __shfl_xor_sync(0xffffffffu, sum[m], 2);
     }
+    __syncthreads();                       // every warp is done with the ring
     // the warps' parts: 16 rows of DV sums, the reference and the sum of weights
     float* mine = as_smem + warp * 16 * (DV + 2);
 #pragma unroll
@@ -202,8 +263,10 @@ __global__ void __launch_bounds__(kAsThreads, DV <= 64 && D <= 64 ? 4 : 3)
         float* r = mine + (8 * m + g) * (DV + 2);
 #pragma unroll
         for (int j = 0; j < CPG; ++j) {
-            r[CPG * 2 * t + j] = o[j][2 * m];
-            r[CPG * (2 * t + 1) + j] = o[j][2 * m + 1];
+            constexpr int PC = CPG < 8 ? CPG : 8;              // channels of a piece
+            const int at = (j / PC) * 8 * PC + j % PC;
+            r[at + PC * 2 * t] = o[j][2 * m];
+            r[at + PC * (2 * t + 1)] = o[j][2 * m + 1];
         }
         if (t == 0) {
             r[DV] = top[m];
