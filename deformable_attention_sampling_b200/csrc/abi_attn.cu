@@ -344,7 +344,7 @@ int mma_backward(const dcnb::AttnArgs& a, const float* scales, int dtype, void* 
             fn = bf16 ? (const void*)dcnb::diff_attn_dkv_mma_kernel<__nv_bfloat16>
                       : (const void*)dcnb::diff_attn_dkv_mma_kernel<__half>;
         }
-        const int rc = launch_attn(fn, f, dim3((unsigned)blocks), dcnb::kAmThreads, smem, stream);
+        const int rc = launch_attn(fn, f, dim3((unsigned)blocks), dcnb::kAbThreads, smem, stream);
         if (rc != DCN_OK) return rc;
     }
     return DCN_OK;

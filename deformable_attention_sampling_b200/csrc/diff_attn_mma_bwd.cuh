@@ -8,8 +8,9 @@
 // goes through atomics; the price is that scores and dP are computed twice
 // (14 of 10 parts of the products' work at D = 64, Dv = 128).
 //
-// Both run 12 warps: 8 compute warps (thread = lane of the accumulators, the
-// two warpgroups take half of a tile's columns each), a producer (tensor-map
+// Both run 20 warps: 16 compute warps (thread = lane of the accumulators, the
+// four warpgroups take a quarter of a tile's columns each; a warp's steps wait
+// for one another, so it takes four a scheduler to keep it busy), a producer (tensor-map
 // loads), a warp that issues the scores and dP of the next tile as soon as the
 // compute warps hold this tile's in registers, a warp that issues the gradient
 // products once their left operands are written, and one that zeroes the rows
@@ -29,6 +30,7 @@
 
 namespace dcnb {
 
+constexpr int kAbThreads = 640;
 constexpr int kAbMaxD = 64;
 constexpr int kAbMaxDv = 128;
 constexpr int kAbRowvBytes = kRowvTile * 4 * 4;
@@ -95,7 +97,7 @@ __device__ __forceinline__ void zero_hidden_rows(unsigned char* tile, int chunk_
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAmThreads, 1)
+__global__ void __launch_bounds__(kAbThreads, 1)
     diff_attn_dq_mma_kernel(const __grid_constant__ AttnBwdArgs f) {
     const AttnArgs& a = f.a;
     const int NS = f.stages;
@@ -136,14 +138,14 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             mbar_init(&kv_clean[s], 1);
         }
         mbar_init(s_full, 1);
-        mbar_init(s_free, 8);
+        mbar_init(s_free, 16);
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&p_full[b], 8);
+            mbar_init(&p_full[b], 16);
             mbar_init(&g_done[b], 1);
         }
         mbar_fence_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
                      :: "r"(smem_u32(tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     // grad_q 64 a map from 320
     const uint32_t d_hi = (uint32_t)(umma_desc128(0, 0) >> 32), lo_k = 16u >> 4 << 16;
 
-    if (warp < 8) {
+    if (warp < 16) {
         // ------------------------------------------------------------- compute
         const int h = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane, tok = q0 + row;
@@ -178,16 +180,16 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         bool ok = true;
         Ring v(NS);
         for (int i = 0; i < count; ++i, v.next()) {
-            const int b = i & 1, j0 = i * kAmKeys + 32 * h;
+            const int b = i & 1, j0 = i * kAmKeys + 16 * h;
             if (a.mask) ok = mbar_wait(&kv_full[v.st], v.phase, f.flags);
             ok = ok && mbar_wait(s_full, (uint32_t)(i & 1), f.flags);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tmem_fence_after();
-            uint32_t r0[32], r1[32], rp[32];
-            tmem_ld32(t_row + 32 * h, r0);
-            tmem_ld32(t_row + 64 + 32 * h, r1);
-            tmem_ld32(t_row + 128 + 32 * h, rp);
+            uint32_t r0[16], r1[16], rp[16];
+            tmem_ld16(t_row + 16 * h, r0);
+            tmem_ld16(t_row + 64 + 16 * h, r1);
+            tmem_ld16(t_row + 128 + 16 * h, rp);
             tmem_wait_ld();
             tmem_fence_before();
             __syncwarp();
@@ -196,18 +198,18 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             float* s1 = reinterpret_cast<float*>(r1);
             const float* dp = reinterpret_cast<const float*>(rp);
             const int in = limit - j0;
-            if (a.mask || !__all_sync(0xffffffffu, in >= 32)) {
-                uint32_t bits = a.mask ? vis[v.st * 2 + h] : 0xffffffffu;
-                bits = in >= 32 ? bits : in <= 0 ? 0u : bits & ((1u << in) - 1u);
+            if (a.mask || !__all_sync(0xffffffffu, in >= 16)) {
+                uint32_t bits = a.mask ? vis[v.st * 2 + (h >> 1)] >> (16 * (h & 1)) : 0xffffu;
+                bits = in >= 16 ? bits : in <= 0 ? 0u : bits & ((1u << in) - 1u);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
+                for (int c = 0; c < 16; ++c) {
                     s0[c] = bits >> c & 1 ? s0[c] : -INFINITY;
                     s1[c] = bits >> c & 1 ? s1[c] : -INFINITY;
                 }
             }
-            uint32_t d0[16], d1[16];
+            uint32_t d0[8], d1[8];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 float2 p0 = __ffma2_rn(make_float2(s0[2 * c], s0[2 * c + 1]), sc2, n0);
                 float2 p1 = __ffma2_rn(make_float2(s1[2 * c], s1[2 * c + 1]), sc2, n1);
                 const float2 g = make_float2(dp[2 * c], dp[2 * c + 1]);
@@ -223,8 +225,8 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tmem_fence_after();
-            tmem_st16(t_row + 192 + 64 * b + 16 * h, d0);
-            tmem_st16(t_row + 192 + 64 * b + 32 + 16 * h, d1);
+            tmem_st8(t_row + 192 + 64 * b + 8 * h, d0);
+            tmem_st8(t_row + 192 + 64 * b + 32 + 8 * h, d1);
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         const float out_scale = a.scale / cs;
         T* dst = static_cast<T*>(a.gq) + (((long long)n * a.Lq + tok) * a.M + head) * 2 * a.D;
         for (int m = 0; m < 2; ++m)
-            for (int c = 16 * h; c < dn; c += 32) {
+            for (int c = 16 * h; c < dn; c += 64) {
                 uint32_t o[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = 0u;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
                 }
                 __syncwarp();
             }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ------------------------------------------------------------ producer
         bool ok = true;
         int loaded = 0;
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         if (count > 0) (void)mbar_wait(q_full, 0, f.flags);
         for (int i = max(0, loaded - NS); i < loaded; ++i)
             (void)mbar_wait(&kv_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ------------------------------------------------------ scores and dP
         const TileProducts t{tmem, d_hi, umma_idesc<T>(kAmKeys, false, f.negate != 0),
                              umma_idesc<T>(kAmKeys, false, false), f.dsteps, f.vsteps};
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             }
             __syncwarp();
         }
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // ------------------------------------------------------------- grad_q
         const uint32_t id_q = umma_idesc<T>(dn, true, false);
         const uint32_t k_s = smem_u32(kvs);
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;"
                      :: "r"(tmem) : "memory");
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
 // Key tiles: lanes are keys, columns the 64 tokens of a query tile; the tiles of
 // all heads that share the key / value head follow one another.
 template <typename T>
-__global__ void __launch_bounds__(kAmThreads, 1)
+__global__ void __launch_bounds__(kAbThreads, 1)
     diff_attn_dkv_mma_kernel(const __grid_constant__ AttnBwdArgs f) {
     constexpr bool kScaled = std::is_same<T, __half>::value;
     const AttnArgs& a = f.a;
@@ -412,12 +414,12 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             mbar_init(&q_empty[s], 1);
         }
         mbar_init(s_full, 1);
-        mbar_init(s_free, 8);
-        mbar_init(p_full, 8);
+        mbar_init(s_free, 16);
+        mbar_init(p_full, 16);
         mbar_init(g_done, 1);
         mbar_fence_init();
     }
-    if (warp == 9) {
+    if (warp == 17) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
                      :: "r"(smem_u32(tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     // 256; grad_v from 384
     const uint32_t d_hi = (uint32_t)(umma_desc128(0, 0) >> 32), lo_k = 16u >> 4 << 16;
 
-    if (warp < 8) {
+    if (warp < 16) {
         // ------------------------------------------------------------- compute
         const int h = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane, key = j0 + row;
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
         for (int i = 0; i < count; ++i, v.next()) {
             const float lam = Elem<T>::one(static_cast<const T*>(a.lam) + head) * cp;
             const float2 lam2 = make_float2(-lam, -lam);
-            const int hidden = from - (t * kAmKeys + 32 * h);      // the first columns, hidden
+            const int hidden = from - (t * kAmKeys + 16 * h);      // the first columns, hidden
             if (++t == qtiles) {
                 t = first;
                 ++head;
@@ -459,10 +461,10 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tmem_fence_after();
-            uint32_t r0[32], r1[32], rp[32];
-            tmem_ld32(t_row + 32 * h, r0);
-            tmem_ld32(t_row + 64 + 32 * h, r1);
-            tmem_ld32(t_row + 128 + 32 * h, rp);
+            uint32_t r0[16], r1[16], rp[16];
+            tmem_ld16(t_row + 16 * h, r0);
+            tmem_ld16(t_row + 64 + 16 * h, r1);
+            tmem_ld16(t_row + 128 + 16 * h, rp);
             tmem_wait_ld();
             tmem_fence_before();
             __syncwarp();
@@ -472,15 +474,15 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             const float* dp = reinterpret_cast<const float*>(rp);
             if (__any_sync(0xffffffffu, hidden > 0)) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
+                for (int c = 0; c < 16; ++c) {
                     s0[c] = c >= hidden ? s0[c] : -INFINITY;
                     s1[c] = c >= hidden ? s1[c] : -INFINITY;
                 }
             }
-            const float* rv = rows + v.st * 4 * kRowvTile + 32 * h;
-            uint32_t d0[16], d1[16], w[16];
+            const float* rv = rows + v.st * 4 * kRowvTile + 16 * h;
+            uint32_t d0[8], d1[8], w[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
                 const float4 l0 = *reinterpret_cast<const float4*>(rv + 4 * c);
                 const float4 l1 = *reinterpret_cast<const float4*>(rv + kRowvTile + 4 * c);
                 const float4 e0 = *reinterpret_cast<const float4*>(rv + 2 * kRowvTile + 4 * c);
@@ -517,11 +519,11 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tmem_fence_after();
-            tmem_st16(t_row + 192 + 16 * h, d0);
-            tmem_st16(t_row + 224 + 16 * h, d1);
+            tmem_st8(t_row + 192 + 8 * h, d0);
+            tmem_st8(t_row + 224 + 8 * h, d1);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<uint4*>(prow + (((4 * h + u) ^ (row & 7)) << 4)) =
+            for (int u = 0; u < 2; ++u)
+                *reinterpret_cast<uint4*>(prow + (((2 * h + u) ^ (row & 7)) << 4)) =
                     make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
             fence_async_shared();
             tmem_wait_st();
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             T* dst = m < 2 ? static_cast<T*>(a.gk) + (at * 2 + m) * a.D
                            : static_cast<T*>(a.gv) + at * a.Dv;
             const float scale = m < 2 ? k_scale : v_scale;
-            for (int c = 16 * h; c < cols; c += 32) {
+            for (int c = 16 * h; c < cols; c += 64) {
                 uint32_t o[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = 0u;
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ------------------------------------------------------------ producer
         if (lane == 0 && count > 0) {
             mbar_arrive_expect_tx(k_full, (uint32_t)((2 + vch) * kAmQBytes));
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
                 (void)mbar_wait(&q_full[i % NS], (uint32_t)((i / NS) & 1), f.flags);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ------------------------------------------------------ scores and dP
         const TileProducts t{tmem, d_hi, umma_idesc<T>(kAmKeys, false, f.negate != 0),
                              umma_idesc<T>(kAmKeys, false, false), f.dsteps, f.vsteps};
@@ -617,7 +619,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
             }
             __syncwarp();
         }
-    } else if (warp == 10) {
+    } else if (warp == 18) {
         // ---------------------------------------------------- grad_k and grad_v
         const uint32_t id_k = umma_idesc<T>(dn, true, false);
         const uint32_t id_v = umma_idesc<T>(dvn, true, false);
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kAmThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;"
                      :: "r"(tmem) : "memory");
