@@ -76,7 +76,7 @@ SIGNATURES = {
     "diff_attn_forward": (_I, [_VP] * 10 + [_LL] + [_I] * 7 + [_LL] * 6 +
                           [ctypes.c_float, _I, _I, _VP]),
     "diff_attn_backward_workspace_size": (_LL, [_I] * 8),
-    "diff_attn_backward": (_I, [_VP] * 15 + [_LL] + [_I] * 7 + [_LL] * 6 +
+    "diff_attn_backward": (_I, [_VP] * 14 + [_LL] + [_I] * 7 + [_LL] * 6 +
                            [ctypes.c_float, _I, _I, _VP]),
     "dcn_output_size": (_I, [_I] * 5),
     "dcn_status_string": (ctypes.c_char_p, [_I]),
@@ -383,12 +383,12 @@ def diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype):
     return int(_load().diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype))
 
 
-def diff_attn_forward(q, k, v, lam, mask, lengths, out, out2, lse, workspace, workspace_bytes, N,
+def diff_attn_forward(q, k, v, lam, mask, lengths, out, maps, lse, workspace, workspace_bytes, N,
                       Lq, Lk, M, Mk, D, Dv, q_image, q_row, k_image, k_row, v_image, v_row, scale,
                       causal, dtype, stream=None):
     """C diff_attn_forward; raises DcnError on a non-OK status."""
     _check(_load().diff_attn_forward(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(mask), _ptr(lengths), _ptr(out), _ptr(out2),
+        _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(mask), _ptr(lengths), _ptr(out), _ptr(maps),
         _ptr(lse), _ptr(workspace), workspace_bytes, N, Lq, Lk, M, Mk, D, Dv, q_image, q_row,
         k_image, k_row, v_image, v_row, scale, causal, dtype, _stream(stream)),
         "diff_attn_forward")
@@ -398,14 +398,14 @@ def diff_attn_backward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype):
     return int(_load().diff_attn_backward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype))
 
 
-def diff_attn_backward(q, k, v, lam, mask, lengths, out, out2, lse, grad_out, grad_q, grad_k,
+def diff_attn_backward(q, k, v, lam, mask, lengths, maps, lse, grad_out, grad_q, grad_k,
                        grad_v, grad_lam, workspace, workspace_bytes, N, Lq, Lk, M, Mk, D, Dv,
                        q_image, q_row, k_image, k_row, v_image, v_row, scale, causal, dtype,
                        stream=None):
     """C diff_attn_backward; raises DcnError on a non-OK status."""
     _check(_load().diff_attn_backward(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(mask), _ptr(lengths), _ptr(out), _ptr(out2),
-        _ptr(lse), _ptr(grad_out), _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(grad_lam),
+        _ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(mask), _ptr(lengths), _ptr(maps), _ptr(lse),
+        _ptr(grad_out), _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(grad_lam),
         _ptr(workspace), workspace_bytes, N, Lq, Lk, M, Mk, D, Dv, q_image, q_row, k_image, k_row,
         v_image, v_row, scale, causal, dtype, _stream(stream)), "diff_attn_backward")
 
@@ -874,19 +874,19 @@ def diff_attn(q, k, v, lam, mask=None, lengths=None, causal=False, scale=None, s
     _require(tuple(out.shape) == (N, Lq, M, Dv) and out.dtype == q.dtype
              and out.device == q.device and out.is_contiguous(),
              "out has the wrong shape, dtype, device or layout")
-    out2 = lse = None
+    maps = lse = None
     if save:
-        out2 = torch.empty((N, Lq, M, Dv), dtype=q.dtype, device=q.device)
+        maps = torch.empty((N, Lq, M, 2, Dv), dtype=torch.float32, device=q.device)
         lse = torch.empty((N, M, 2, Lq), dtype=torch.float32, device=q.device)
     with _on_device(q):
         need = diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, code)
         if need < 0:
             raise DcnError(need, "diff_attn_forward_workspace_size")
         ws, ws_bytes = _workspace(need, q.device, workspace)
-        diff_attn_forward(q, k, v, lam, mask, lengths, out, out2, lse, ws, ws_bytes, N, Lq, Lk, M,
+        diff_attn_forward(q, k, v, lam, mask, lengths, out, maps, lse, ws, ws_bytes, N, Lq, Lk, M,
                           Mk, D, Dv, *strides, D ** -0.5 if scale is None else scale,
                           int(bool(causal)), code, stream)
-    return (out, (out2, lse)) if save else out
+    return (out, (maps, lse)) if save else out
 
 
 def diff_attn_grad(q, k, v, lam, out, saved, grad_out, mask=None, lengths=None, causal=False,
@@ -896,13 +896,14 @@ def diff_attn_grad(q, k, v, lam, out, saved, grad_out, mask=None, lengths=None, 
     import torch
     (N, Lq, Lk, M, Mk, D, Dv), strides = _attn_checks(q, k, v, lam, mask, lengths)
     code = dtype_code(q)
-    out2, lse = saved
-    _same_device(q, out, out2, lse, grad_out)
-    for t in (out, out2, grad_out):
+    maps, lse = saved
+    _same_device(q, out, maps, lse, grad_out)
+    for t in (out, grad_out):
         _require(tuple(t.shape) == (N, Lq, M, Dv) and t.dtype == q.dtype and t.is_contiguous(),
-                 "out, saved and grad_out must be contiguous [N, Lq, M, Dv] of q's dtype")
-    _require(tuple(lse.shape) == (N, M, 2, Lq) and lse.dtype == torch.float32
-             and lse.is_contiguous(), "saved must be diff_attn's")
+                 "out and grad_out must be contiguous [N, Lq, M, Dv] of q's dtype")
+    for t, shape in ((maps, (N, Lq, M, 2, Dv)), (lse, (N, M, 2, Lq))):
+        _require(tuple(t.shape) == shape and t.dtype == torch.float32 and t.is_contiguous(),
+                 "saved must be diff_attn's")
     gq = torch.empty((N, Lq, M, 2, D), dtype=q.dtype, device=q.device)
     gk = torch.empty((N, Lk, Mk, 2, D), dtype=q.dtype, device=q.device)
     gv = torch.empty((N, Lk, Mk, Dv), dtype=q.dtype, device=q.device)
@@ -912,7 +913,7 @@ def diff_attn_grad(q, k, v, lam, out, saved, grad_out, mask=None, lengths=None, 
         if need < 0:
             raise DcnError(need, "diff_attn_backward_workspace_size")
         ws, ws_bytes = _workspace(need, q.device, workspace)
-        diff_attn_backward(q, k, v, lam, mask, lengths, out, out2, lse, grad_out, gq, gk, gv, gl,
+        diff_attn_backward(q, k, v, lam, mask, lengths, maps, lse, grad_out, gq, gk, gv, gl,
                            ws, ws_bytes, N, Lq, Lk, M, Mk, D, Dv, *strides,
                            D ** -0.5 if scale is None else scale, int(bool(causal)), code, stream)
     return gq, gk, gv, gl

@@ -411,7 +411,7 @@ long long diff_attn_forward_workspace_size(int N, int Lq, int Lk, int M, int Mk,
 }
 
 int diff_attn_forward(const void* q, const void* k, const void* v, const void* lambda,
-                      const unsigned char* mask, const int* lengths, void* out, void* out2,
+                      const unsigned char* mask, const int* lengths, void* out, float* maps,
                       float* lse, void* workspace, long long workspace_bytes, int N, int Lq, int Lk,
                       int M, int Mk, int D, int Dv, long long q_image, long long q_row,
                       long long k_image, long long k_row, long long v_image, long long v_row,
@@ -423,24 +423,24 @@ int diff_attn_forward(const void* q, const void* k, const void* v, const void* l
     if (N == 0 || Lq == 0) return DCN_OK;
     const int es = elem_bytes(dtype);
     if ((rc = attn_pointers(a, es)) != DCN_OK) return rc;
-    if (!out || (out2 == nullptr) != (lse == nullptr)) return DCN_ERR_INVALID_ARG;
-    if (((uintptr_t)out | (uintptr_t)out2) % es != 0 || (uintptr_t)lse % 4 != 0 ||
+    if (!out || (maps == nullptr) != (lse == nullptr)) return DCN_ERR_INVALID_ARG;
+    if ((uintptr_t)out % es != 0 || ((uintptr_t)maps | (uintptr_t)lse) % 4 != 0 ||
         (uintptr_t)workspace % 16 != 0)
         return DCN_ERR_MISALIGNED;
     const AttnPlan p = attn_plan(N, Lq, Lk, M, Mk);
     const bool mma = mma_sizes(dtype, D, Dv) && Lq >= kMmaMinTokens && mma_layout(a) &&
-                     ((uintptr_t)out | (uintptr_t)out2) % 16 == 0;
+                     ((uintptr_t)out | (uintptr_t)maps) % 16 == 0;
     const bool step = step_sizes(dtype, D, Dv) && Lq < kMmaMinTokens && mma_layout(a);
     const long long need = diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return DCN_ERR_INVALID_ARG;
     const long long ob = (long long)N * Lq * M * Dv * es;
     Span ins[kInputs];
     input_spans(a, es, ins);
-    const Span outs[] = {{out, ob}, {out2, ob}, {lse, (long long)N * M * 2 * Lq * 4},
+    const Span outs[] = {{out, ob}, {maps, ob / es * 8}, {lse, (long long)N * M * 2 * Lq * 4},
                          {workspace, need}};
     if (any_clash(outs, 4, ins, kInputs)) return DCN_ERR_INVALID_ARG;
     a.out = out;
-    a.out2 = out2;
+    a.maps = maps;
     a.lse = lse;
     a.splits = mma    ? mma_splits(N, Lq, Lk, M, Dv)
                : step ? step_splits(N, Lq, Lk, M, Mk)
@@ -492,8 +492,8 @@ long long diff_attn_backward_workspace_size(int N, int Lq, int Lk, int M, int Mk
 }
 
 int diff_attn_backward(const void* q, const void* k, const void* v, const void* lambda,
-                       const unsigned char* mask, const int* lengths, const void* out,
-                       const void* out2, const float* lse, const void* grad_out, void* grad_q,
+                       const unsigned char* mask, const int* lengths, const float* maps,
+                       const float* lse, const void* grad_out, void* grad_q,
                        void* grad_k, void* grad_v, void* grad_lambda, void* workspace,
                        long long workspace_bytes, int N, int Lq, int Lk, int M, int Mk, int D,
                        int Dv, long long q_image, long long q_row, long long k_image,
@@ -508,26 +508,25 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
     if (!grad_lambda) return DCN_ERR_INVALID_ARG;
     if (tokens > 0) {
         if ((rc = attn_pointers(a, es)) != DCN_OK) return rc;
-        if (!out || !out2 || !lse || !grad_out || !grad_q || !workspace) return DCN_ERR_INVALID_ARG;
+        if (!maps || !lse || !grad_out || !grad_q || !workspace) return DCN_ERR_INVALID_ARG;
     }
     if (keys > 0 && (!grad_k || !grad_v)) return DCN_ERR_INVALID_ARG;
-    if (((uintptr_t)out | (uintptr_t)out2 | (uintptr_t)grad_out | (uintptr_t)grad_q |
+    if (((uintptr_t)grad_out | (uintptr_t)grad_q |
          (uintptr_t)grad_k | (uintptr_t)grad_v | (uintptr_t)grad_lambda) % es != 0 ||
-        ((uintptr_t)lse | (uintptr_t)lengths) % 4 != 0 || (uintptr_t)workspace % 16 != 0)
+        ((uintptr_t)lse | (uintptr_t)maps | (uintptr_t)lengths) % 4 != 0 || (uintptr_t)workspace % 16 != 0)
         return DCN_ERR_MISALIGNED;
     const long long need = diff_attn_backward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, dtype);
     if (workspace_bytes < need) return DCN_ERR_INVALID_ARG;
     const long long ob = tokens * M * Dv * es, sb = tokens * M * 2 * 4;
-    Span ins[kInputs + 4];
+    Span ins[kInputs + 3];
     input_spans(a, es, ins);
-    ins[kInputs] = {out, ob};
-    ins[kInputs + 1] = {out2, ob};
-    ins[kInputs + 2] = {lse, sb};
-    ins[kInputs + 3] = {grad_out, ob};
+    ins[kInputs] = {maps, ob / es * 8};
+    ins[kInputs + 1] = {lse, sb};
+    ins[kInputs + 2] = {grad_out, ob};
     const Span outs[] = {{grad_q, tokens * M * 2 * D * es}, {grad_k, keys * Mk * 2 * D * es},
                          {grad_v, keys * Mk * Dv * es}, {grad_lambda, (long long)M * es},
                          {workspace, need}};
-    if (any_clash(outs, 5, ins, kInputs + 4)) return DCN_ERR_INVALID_ARG;
+    if (any_clash(outs, 5, ins, kInputs + 3)) return DCN_ERR_INVALID_ARG;
     a.vec4 = a.vec4 && (uintptr_t)grad_out % (uintptr_t)(4 * es) == 0;
     a.go = grad_out;
     a.lse = const_cast<float*>(lse);
@@ -563,16 +562,15 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
     float* const ws = static_cast<float*>(workspace);
     dcnb::AttnDeltaArgs d = {};
     d.a = a;
-    d.out = out;
-    d.out2 = out2;
+    d.maps = maps;
     d.go = grad_out;
     d.lam = lambda;
     d.lse = lse;
     d.rowv = ws;
     d.scales = ws + rowv_floats(N, Lq, M);
     d.glam = grad_lambda;
-    d.vec4 = Dv % 4 == 0 &&
-             ((uintptr_t)out | (uintptr_t)out2 | (uintptr_t)grad_out) % (uintptr_t)(4 * es) == 0;
+    d.vec4 = Dv % 4 == 0 && (uintptr_t)maps % 16 == 0 &&
+             (uintptr_t)grad_out % (uintptr_t)(4 * es) == 0;
     const long long g_blocks = rowv_floats(N, Lq, M) / (4 * 8);
     const long long v_blocks = mma && dtype == DCN_F16 ? (keys * Mk + 7) / 8 : 0;
     if (g_blocks + v_blocks > kInt31) return DCN_ERR_UNSUPPORTED;

@@ -41,7 +41,7 @@ struct AttnArgs {
     const unsigned char* mask;     // [N][Lk], non-zero = masked, or null
     const int* lengths;            // [N] or null
     void* out;
-    void* out2;                    // second map's part, or null
+    float* maps;                   // [N][Lq][M][2][Dv], the maps' own outputs, or null
     float* lse;                    // [N][M][2][Lq], or null
     float* part_ml;                // [splits][N * Mk * rows][2][2]
     float* part_o;                 // [splits][N * Mk * rows][2][Dv]
@@ -61,6 +61,12 @@ struct AttnArgs {
     long long q_image, q_row, k_image, k_row, v_image, v_row;
     FastDiv div_G, div_Mk;
 };
+
+// O_0 - lambda O_1, with the same roundings whether the maps' outputs are stored
+// or not (a contraction with the product before would differ).
+__device__ __forceinline__ float attn_diff(float o0, float lam, float o1) {
+    return fmaf(-lam, o1, o0);
+}
 
 __device__ __forceinline__ int attn_len(const AttnArgs& a, int n) {
     return a.lengths ? max(0, min(a.lengths[n], a.Lk)) : a.Lk;
@@ -354,9 +360,12 @@ __global__ void __launch_bounds__(kAttnThreads) diff_attn_kernel(const AttnArgs 
         for (int c = 0; c < CT; ++c) {
             const int col = attn_col<CT>(c);
             if (col >= Dv) continue;
-            const float second = o[1][r][c] * i1;
-            static_cast<T*>(a.out)[at + col] = Elem<T>::from(o[0][r][c] * i0 - lam * second);
-            if (a.out2) static_cast<T*>(a.out2)[at + col] = Elem<T>::from(second);
+            const float one = __fmul_rn(o[0][r][c], i0), second = __fmul_rn(o[1][r][c], i1);
+            static_cast<T*>(a.out)[at + col] = Elem<T>::from(attn_diff(one, lam, second));
+            if (a.maps) {
+                a.maps[2 * at + col] = one;
+                a.maps[2 * at + Dv + col] = second;
+            }
         }
         if (a.lse && tx < 2) {
             const float ms = tx ? m[1][r] : m[0][r], ls = tx ? l[1][r] : l[0][r];
@@ -421,9 +430,13 @@ __global__ void __launch_bounds__(kJoinThreads) diff_attn_join_kernel(const Attn
             x = fmaf(weight[0][sp], p[0], x);
             y = fmaf(weight[1][sp], p[Dv], y);
         }
-        y *= inv[1];
-        static_cast<T*>(a.out)[to + c] = Elem<T>::from(x * inv[0] - lam * y);
-        if (a.out2) static_cast<T*>(a.out2)[to + c] = Elem<T>::from(y);
+        x = __fmul_rn(x, inv[0]);
+        y = __fmul_rn(y, inv[1]);
+        static_cast<T*>(a.out)[to + c] = Elem<T>::from(attn_diff(x, lam, y));
+        if (a.maps) {
+            a.maps[2 * to + c] = x;
+            a.maps[2 * to + Dv + c] = y;
+        }
     }
 }
 
@@ -440,10 +453,9 @@ __global__ void __launch_bounds__(kJoinThreads) diff_attn_join_kernel(const Attn
 // depend on the order of blocks.
 
 struct AttnDeltaArgs {
-    const void* out;
-    const void* out2;
+    const float* maps;
     const void* go;
-    const void* lam;
+    const void* lam;       // second kernel
     const float* lse;
     AttnArgs a;            // geometry, visible keys and v
     float* rowv;
@@ -451,12 +463,14 @@ struct AttnDeltaArgs {
     float* peak;           // [blocks] largest |g|^2 and |v|^2 of a block, or null
     float* scales;         // cs, cp
     int g_blocks, v_blocks;
-    int vec4;              // rows of out, out2 and grad_out are aligned groups of 4
+    int vec4;              // rows of the maps and of grad_out are aligned groups of 4
 };
 
-// One warp per (token, head), tokens padded to whole tiles: e_1 = <g, O_1> from
-// the saved second part, e_0 = <g, O_0> = <g, out> + lambda e_1.  Rows past the
-// end and rows that see no key get -lse = -inf: weights of 0.
+// One warp per (token, head), tokens padded to whole tiles: e_s = <g, O_s> from
+// the maps' own outputs, kept in float32 (with outputs rounded to 16 bits the
+// differences dP - e_s, and with them grad_q, grad_k and grad_lambda, carried
+// that rounding: grad_lambda was off by up to twice a 16-bit result's own).
+// Rows past the end and rows that see no key get -lse = -inf: weights of 0.
 // With `peak` the blocks also find the largest |g|^2 and, in blocks of their
 // own, the largest |v|^2 of a visible key.
 template <typename T>
@@ -477,13 +491,12 @@ __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArg
             if (i < a.Lq) {
                 const long long row = (((long long)n * a.Lq + i) * a.M + h) * a.Dv;
                 const T* g = static_cast<const T*>(d.go) + row;
-                const T* o = static_cast<const T*>(d.out) + row;
-                const T* o2 = static_cast<const T*>(d.out2) + row;
+                const float* o = d.maps + 2 * row;
                 // four channels a lane where rows are aligned groups of four
                 for (int c = 4 * lane; c < a.Dv; c += 128) {
                     const float4 gv = attn_ld4<T>(g, c, a.Dv, d.vec4);
-                    const float4 ov = attn_ld4<T>(o, c, a.Dv, d.vec4);
-                    const float4 o2v = attn_ld4<T>(o2, c, a.Dv, d.vec4);
+                    const float4 ov = attn_ld4<float>(o, c, a.Dv, d.vec4);
+                    const float4 o2v = attn_ld4<float>(o + a.Dv, c, a.Dv, d.vec4);
                     s = dot4(s, gv, ov);
                     s2 = dot4(s2, gv, o2v);
                     peak = dot4(peak, gv, gv);
@@ -498,8 +511,7 @@ __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArg
             float* r = d.rowv + attn_rowv(a, n, h, i);
             if (lane < 2) {
                 r[lane * kRowvTile] = -lse;
-                const float lam = Elem<T>::one(static_cast<const T*>(d.lam) + h);
-                r[(2 + lane) * kRowvTile] = lane ? -s2 : -(s + lam * s2);
+                r[(2 + lane) * kRowvTile] = lane ? -s2 : -s;
             }
         }
     } else {

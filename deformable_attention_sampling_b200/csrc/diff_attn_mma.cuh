@@ -314,17 +314,24 @@ __global__ void __launch_bounds__(kAmThreads, 1)
                             make_uint4(o1[e], o1[e + 1], o1[e + 2], o1[e + 3]);
                     }
             } else if (live) {
-                float x[16], y[16];
+                float x[16], y[16], z[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    y[e] = __uint_as_float(o1[e]) * i1;
-                    x[e] = __uint_as_float(o0[e]) * i0 - lam * y[e];
+                    x[e] = __fmul_rn(__uint_as_float(o0[e]), i0);
+                    y[e] = __fmul_rn(__uint_as_float(o1[e]), i1);
+                    z[e] = attn_diff(x[e], lam, y[e]);
                 }
 #pragma unroll
                 for (int e = 0; e < 16; e += 8)
                     if (c + e < dv) {
-                        st_f32<T, 8>(static_cast<T*>(a.out) + to + c + e, x + e);
-                        if (a.out2) st_f32<T, 8>(static_cast<T*>(a.out2) + to + c + e, y + e);
+                        st_f32<T, 8>(static_cast<T*>(a.out) + to + c + e, z + e);
+                        if (a.maps) {
+                            float* d = a.maps + 2 * to - c0 + c + e;
+                            st_f32<float, 4>(d, x + e);
+                            st_f32<float, 4>(d + 4, x + e + 4);
+                            st_f32<float, 4>(d + a.Dv, y + e);
+                            st_f32<float, 4>(d + a.Dv + 4, y + e + 4);
+                        }
                     }
             }
             __syncwarp();

@@ -310,9 +310,13 @@ __global__ void __launch_bounds__(kAsThreads, D == 128 && DV == 128 ? 2 : DV <= 
                 a.part_o[at * 2 * DV + c] = x;
                 a.part_o[(at * 2 + 1) * DV + c] = y;
             } else {
-                y *= i1;
-                static_cast<T*>(a.out)[to + c] = Elem<T>::from(x * i0 - lam * y);
-                if (a.out2) static_cast<T*>(a.out2)[to + c] = Elem<T>::from(y);
+                x = __fmul_rn(x, i0);
+                y = __fmul_rn(y, i1);
+                static_cast<T*>(a.out)[to + c] = Elem<T>::from(attn_diff(x, lam, y));
+                if (a.maps) {
+                    a.maps[2 * to + c] = x;
+                    a.maps[2 * to + DV + c] = y;
+                }
             }
         }
         if (lane < 2) {

@@ -613,7 +613,7 @@ DCN_API int norm_residual_backward(const void* y, const void* z, const void* gra
  *   lambda [M]; mask [N][Lk] bytes or NULL; lengths [N] int32 or NULL (Lk)
  *   out [N][Lq][M][Dv], dense
  * For the backward pass the call also stores (both or neither, else NULL)
- *   out2 [N][Lq][M][Dv] dense, the second map's own output sum_j P_1 v
+ *   maps [N][Lq][M][2][Dv] float32, dense, the maps' own outputs sum_j P_s v
  *   lse  [N][M][2][Lq] float32, log2 of the sum of exponentials of each map's
  *        scores, +inf for a token that sees no key
  * Scores, softmax statistics and sums are float32; with 16-bit data on the
@@ -628,7 +628,7 @@ DCN_API int norm_residual_backward(const void* y, const void* z, const void* gra
  * null pointer, a small workspace or an overlapping output; DCN_ERR_MISALIGNED.
  */
 DCN_API int diff_attn_forward(const void* q, const void* k, const void* v, const void* lambda,
-                      const unsigned char* mask, const int* lengths, void* out, void* out2,
+                      const unsigned char* mask, const int* lengths, void* out, float* maps,
                       float* lse, void* workspace, long long workspace_bytes, int N, int Lq,
                       int Lk, int M, int Mk, int D, int Dv, long long q_image, long long q_row,
                       long long k_image, long long k_row, long long v_image, long long v_row,
@@ -646,16 +646,16 @@ DCN_API long long diff_attn_backward_workspace_size(int N, int Lq, int Lk, int M
 
 /*
  * diff_attn_backward - gradients of diff_attn_forward with respect to q, k, v
- * and lambda, from its inputs, its outputs out, out2 and lse, and grad_out
- * (dense, as out).  The gradients are dense: grad_q [N][Lq][M][2][D], grad_k
+ * and lambda, from its inputs, its outputs maps and lse, and grad_out (dense,
+ * as out).  The gradients are dense: grad_q [N][Lq][M][2][D], grad_k
  * [N][Lk][Mk][2][D], grad_v [N][Lk][Mk][Dv], grad_lambda [M]; those of a key /
  * value head are summed over its M / Mk heads.  Keys that no token sees get
  * zeros.  No sum goes through atomics: equal calls give equal bits.
  * Arguments, limits and errors otherwise as diff_attn_forward.
  */
 DCN_API int diff_attn_backward(const void* q, const void* k, const void* v, const void* lambda,
-                       const unsigned char* mask, const int* lengths, const void* out,
-                       const void* out2, const float* lse, const void* grad_out, void* grad_q,
+                       const unsigned char* mask, const int* lengths, const float* maps,
+                       const float* lse, const void* grad_out, void* grad_q,
                        void* grad_k, void* grad_v, void* grad_lambda, void* workspace,
                        long long workspace_bytes, int N, int Lq, int Lk, int M, int Mk, int D,
                        int Dv, long long q_image, long long q_row, long long k_image,

@@ -98,7 +98,7 @@ def visible(N, Lq, Lk, mask, lengths, causal):
 
 
 def attn(q, k, v, lam, mask=None, lengths=None, causal=False, scale=None, grad_out=None):
-    """Dict name -> (value, bound): out, out2, lse and, with grad_out, q, k, v, lam."""
+    """Dict name -> (value, bound): out, maps, lse and, with grad_out, q, k, v, lam."""
     dt = q.dtype
     N, Lq, M, _, D = q.shape
     Lk, Mk, Dv = v.shape[1:]
@@ -138,17 +138,15 @@ def attn(q, k, v, lam, mask=None, lengths=None, causal=False, scale=None, grad_o
     lse = ((top + torch.log(tot)) * math.log2(math.e))[..., 0]     # [N,Mk,G,2,Lq]
     lse = torch.where(tot[..., 0] > 0, lse, torch.full_like(lse, math.inf)).reshape(N, M, 2, Lq)
     blse = ((2 * ds[..., 0] + (Lk + 24) * U) * 1.5).reshape(N, M, 2, Lq) + 4 * U * lse.abs()
-    r = {"out": (heads(out), heads(bout)), "out2": (heads(o1), heads(b1)), "lse": (lse, blse)}
+    r = {"out": (heads(out), heads(bout)), "maps": (torch.stack([heads(o0), heads(o1)], 3), torch.stack([heads(b0), heads(b1)], 3)), "lse": (lse, blse)}
     if grad_out is None:
         return r
     g = f64(grad_out).view(N, Lq, Mk, G, Dv).permute(0, 2, 3, 1, 4)
     dp, mdp = g @ V.transpose(-1, -2), g.abs() @ V.abs().transpose(-1, -2)
     e = torch.stack([(g * o0).sum(-1), (g * o1).sum(-1)], 3)[..., None]          # [N,Mk,G,2,Lq,1]
-    # the saved outputs are rounded to the type
-    s1 = b1 + half(dt) * o1.abs()
-    s0 = bout + half(dt) * out.abs() + l.abs() * s1
+    s1, s0 = b1 + 2 * U * o1.abs(), b0 + 2 * U * o0.abs()       # the saved outputs are float32
     be = torch.stack([(g.abs() * s0).sum(-1), (g.abs() * s1).sum(-1)], 3)[..., None]
-    be = be + (Dv + 8) * U * torch.stack([(g.abs() * (o0.abs() + 2 * (l * o1).abs())).sum(-1),
+    be = be + (Dv + 8) * U * torch.stack([(g.abs() * o0.abs()).sum(-1),
                                           (g.abs() * o1.abs()).sum(-1)], 3)[..., None]
     sign = torch.stack([torch.ones_like(l), -l], 2)                              # [Mk,G,2,1,1]
     x = dp[:, :, :, None] - e

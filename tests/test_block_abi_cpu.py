@@ -128,7 +128,7 @@ def test_norm_residual_empty_forward(lib):
 
 
 def attn(lib, grad=False, **kw):
-    a = dict(q=P[0], k=P[1], v=P[2], lam=P[3], mask=P[4], lengths=P[5], out=P[6], out2=P[7],
+    a = dict(q=P[0], k=P[1], v=P[2], lam=P[3], mask=P[4], lengths=P[5], out=P[6], maps=P[7],
              lse=P[8], go=P[9], gq=P[10], gk=P[11], gv=P[12], gl=P[13], ws=P[14],
              ws_bytes=1 << 33, N=2, Lq=9, Lk=70, M=4, Mk=2, D=64, Dv=128, scale=0.125, causal=1,
              dtype=BF16)
@@ -139,10 +139,10 @@ def attn(lib, grad=False, **kw):
                                       ("k_image", a["Lk"] * kr), ("k_row", kr),
                                       ("v_image", a["Lk"] * vr), ("v_row", vr))]
     tail += [a["scale"], a["causal"], a["dtype"], None]
-    head = [a[k] for k in ("q", "k", "v", "lam", "mask", "lengths", "out", "out2", "lse")]
+    head = [a[k] for k in ("q", "k", "v", "lam", "mask", "lengths")]
     if grad:
-        return lib.diff_attn_backward(*head, a["go"], a["gq"], a["gk"], a["gv"], a["gl"], *tail)
-    return lib.diff_attn_forward(*head, *tail)
+        return lib.diff_attn_backward(*head, a["maps"], a["lse"], a["go"], a["gq"], a["gk"], a["gv"], a["gl"], *tail)
+    return lib.diff_attn_forward(*head, a["out"], a["maps"], a["lse"], *tail)
 
 
 @pytest.mark.parametrize("grad", [False, True])
@@ -154,8 +154,8 @@ def attn(lib, grad=False, **kw):
     (dict(D=129), UNSUP), (dict(Dv=257), UNSUP), (dict(N=40000, Lq=1, Lk=1), UNSUP),
     (dict(Lk=2147483647, Lq=1), UNSUP), (dict(Lq=1 << 30), UNSUP),
     (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(lam=None), BAD),
-    (dict(out=None), BAD), (dict(q=P[0] + 1), ALIGN), (dict(lengths=P[5] + 2), ALIGN),
-    (dict(lse=P[8] + 2), ALIGN), (dict(ws=P[14] + 8), ALIGN), (dict(out2=P[7] + 1), ALIGN),
+    (dict(q=P[0] + 1), ALIGN), (dict(lengths=P[5] + 2), ALIGN),
+    (dict(lse=P[8] + 2), ALIGN), (dict(ws=P[14] + 8), ALIGN), (dict(maps=P[7] + 2), ALIGN),
 ])
 def test_diff_attn_refusals(lib, grad, change, status):
     before = dcnb.dcn_launch_count()
@@ -164,16 +164,17 @@ def test_diff_attn_refusals(lib, grad, change, status):
 
 
 @pytest.mark.parametrize("change", [
-    dict(out2=None), dict(lse=None), dict(out=P[0] + 64), dict(out=P[1]), dict(out2=P[6]),
+    dict(out=None), dict(maps=None), dict(lse=None), dict(out=P[0] + 64), dict(out=P[1]),
+    dict(maps=P[6]),
     dict(lse=P[4]), dict(out=P[3])])
 def test_diff_attn_forward_pointers(lib, change):
     assert attn(lib, **change) == BAD
 
 
 @pytest.mark.parametrize("change", [
-    dict(go=None), dict(gq=None), dict(gk=None), dict(gv=None), dict(gl=None), dict(out2=None),
+    dict(go=None), dict(gq=None), dict(gk=None), dict(gv=None), dict(gl=None), dict(maps=None),
     dict(lse=None), dict(ws=None), dict(ws_bytes=16), dict(gq=P[0]), dict(gk=P[2] + 16),
-    dict(gv=P[9]), dict(gl=P[8]), dict(gq=P[11]), dict(ws=P[6])])
+    dict(gv=P[9]), dict(gl=P[8]), dict(gq=P[11]), dict(ws=P[7])])
 def test_diff_attn_backward_pointers(lib, change):
     assert attn(lib, True, **change) == BAD
 

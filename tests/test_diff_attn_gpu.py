@@ -31,7 +31,7 @@ def run_and_check(q, k, v, lam, go, grad=True, **kw):
     out, saved = dcnb.diff_attn(q, k, v, lam, save=True, **kw)
     r = ref.attn(q, k, v, lam, grad_out=go if grad else None, **kw)
     ref.check(out, *r["out"], "out")
-    ref.check(saved[0], *r["out2"], "out2")
+    ref.check(saved[0], *r["maps"], "maps")
     want, bound = r["lse"]
     got = saved[1].double().cpu()
     empty = torch.isinf(want)
