@@ -306,8 +306,12 @@ long long rowv_floats(int N, int Lq, int M) {
     return (long long)N * M * ceil_div(Lq, dcnb::kRowvTile) * 4 * dcnb::kRowvTile;
 }
 
-int mma_backward(const dcnb::AttnArgs& a, const float* scales, int dtype, void* stream) {
+// Row values (and fp16's scales) are set; `glam` sums grad_lambda from the row
+// values between the two kernels: the first one refines them.
+int mma_backward(const dcnb::AttnArgs& a, const float* scales, float* rowv, const void* glam,
+                 const dcnb::AttnDeltaArgs& d, int dtype, void* stream) {
     dcnb::AttnBwdArgs f;
+    f.rowv = rowv;
     f.a = a;
     f.negate = a.scale < 0.f ? 1 : 0;
     f.a.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-30f);
@@ -344,7 +348,8 @@ int mma_backward(const dcnb::AttnArgs& a, const float* scales, int dtype, void* 
             fn = bf16 ? (const void*)dcnb::diff_attn_dkv_mma_kernel<__nv_bfloat16>
                       : (const void*)dcnb::diff_attn_dkv_mma_kernel<__half>;
         }
-        const int rc = launch_attn(fn, f, dim3((unsigned)blocks), dcnb::kAbThreads, smem, stream);
+        int rc = launch_attn(fn, f, dim3((unsigned)blocks), dcnb::kAbThreads, smem, stream);
+        if (rc == DCN_OK && pass == 0) rc = launch_grid(glam, d, a.M, 1024, 0, stream);
         if (rc != DCN_OK) return rc;
     }
     return DCN_OK;
@@ -581,10 +586,17 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
         rc = launch_grid(delta, d, (int)(g_blocks + v_blocks), 256, 0, stream);
         if (rc != DCN_OK) return rc;
     }
-    // zeros for an empty batch; one block more for the scales
-    rc = launch_grid(glam, d, mma ? M + 1 : M, 1024, 0, stream);
+    if (mma) {
+        if (d.peak) {
+            dcnb::AttnDeltaArgs scales = d;
+            scales.first_block = M;
+            rc = launch_grid(glam, scales, 1, 1024, 0, stream);
+            if (rc != DCN_OK) return rc;
+        }
+        return mma_backward(a, d.scales, ws, glam, d, dtype, stream);
+    }
+    rc = launch_grid(glam, d, M, 1024, 0, stream);       // zeros for an empty batch
     if (rc != DCN_OK) return rc;
-    if (mma) return mma_backward(a, d.scales, dtype, stream);
     const int use_ct = bt == 32 && cd <= 4 ? 16 : ct;
     const int smem = dcnb::attn_bwd_smem(bt, cd, use_ct);
     if (tokens > 0) {

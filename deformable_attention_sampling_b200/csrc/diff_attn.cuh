@@ -463,6 +463,7 @@ struct AttnDeltaArgs {
     float* peak;           // [blocks] largest |g|^2 and |v|^2 of a block, or null
     float* scales;         // cs, cp
     int g_blocks, v_blocks;
+    int first_block;       // of the second kernel: its blocks count from here
     int vec4;              // rows of the maps and of grad_out are aligned groups of 4
 };
 
@@ -546,16 +547,16 @@ __device__ __forceinline__ float attn_pow2(float x) {
     return exp2f(fminf(fmaxf(15.f - ceilf(log2f(x)), -40.f), 40.f));
 }
 
-// grad_lambda of head blockIdx.x: one block, a fixed order.  One block more sets
-// the scales of the tensor-core kernels' fp16 operands from the blocks' peaks.
+// Block h: grad_lambda of head h, in a fixed order.  Block M sets the scales of
+// the tensor-core kernels' fp16 operands from the delta kernel's peaks.
 template <typename T>
 __global__ void __launch_bounds__(1024) diff_attn_glam_kernel(const AttnDeltaArgs d) {
     __shared__ float part[32][3];
     const AttnArgs& a = d.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)blockIdx.x == a.M) {
+    if ((int)blockIdx.x + d.first_block == a.M) {
         float x[3] = {0.f, 0.f, 0.f};
-        if (d.peak) {
+        {
             for (int i = threadIdx.x; i < d.g_blocks + d.v_blocks; i += 1024) {
                 const int k = i < d.g_blocks ? 0 : 1;
                 x[k] = fmaxf(x[k], d.peak[i]);
@@ -575,9 +576,9 @@ __global__ void __launch_bounds__(1024) diff_attn_glam_kernel(const AttnDeltaArg
                 for (int k = 0; k < 3; ++k) part[0][k] = fmaxf(part[0][k], part[w][k]);
             const float lam = part[0][2];
             // |dS| <= 2 max(1, |lambda|) |g| |v|, |P_0 - lambda P_1| <= 1 + |lambda|
-            d.scales[0] = d.peak ? attn_pow2(2.f * fmaxf(1.f, lam) * sqrtf(part[0][0]) *
-                                             sqrtf(part[0][1])) : 1.f;
-            d.scales[1] = d.peak ? attn_pow2(1.f + lam) : 1.f;
+            d.scales[0] = attn_pow2(2.f * fmaxf(1.f, lam) * sqrtf(part[0][0]) *
+                                    sqrtf(part[0][1]));
+            d.scales[1] = attn_pow2(1.f + lam);
         }
         return;
     }

@@ -41,7 +41,8 @@ struct AttnBwdArgs {
     CUtensorMap tv;            // [N][Lk][Mk][Dv]
     CUtensorMap tg;            // [N][Lq][M][Dv]
     AttnArgs a;
-    const float* scales;       // cs, cp
+    const float* scales;       // cs, cp (fp16)
+    float* rowv;               // the row values, whose e_s the first kernel rewrites
     unsigned int* flags;
     int dsteps, vsteps;        // K = 16 steps of a head, of the values
     int stages;
@@ -50,7 +51,7 @@ struct AttnBwdArgs {
 };
 
 __host__ __device__ constexpr int attn_dq_smem(int vch, int stages) {
-    return 1024 + (2 + vch) * kAmQBytes + stages * (2 + vch) * kAmKBytes + 1024;
+    return 1024 + (2 + vch) * kAmQBytes + stages * (2 + vch) * kAmKBytes + 1024 + 4096;
 }
 __host__ __device__ constexpr int attn_dkv_smem(int vch, int stages) {
     return 1024 + (3 + vch) * kAmQBytes + stages * ((2 + vch) * kAmKBytes + kAbRowvBytes) +
@@ -99,6 +100,7 @@ __device__ __forceinline__ void zero_hidden_rows(unsigned char* tile, int chunk_
 template <typename T>
 __global__ void __launch_bounds__(kAbThreads, 1)
     diff_attn_dq_mma_kernel(const __grid_constant__ AttnBwdArgs f) {
+    constexpr bool kScaled = std::is_same<T, __half>::value;
     const AttnArgs& a = f.a;
     const int NS = f.stages;
     extern __shared__ __align__(128) unsigned char am_smem[];
@@ -129,6 +131,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     uint64_t* g_done = p_full + 2;        // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g_done + 2);
     uint32_t* vis = tmem_slot + 4;        // [NS][2]
+    float2* esum = reinterpret_cast<float2*>(vis + 2 * NS);       // [4][128]
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -164,7 +167,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const int row = quarter * 32 + lane, tok = q0 + row;
         const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
         const int limit = a.causal ? min(len, tok + len - a.Lq + 1) : len;
-        const float cs = f.scales[0], lam = Elem<T>::one(static_cast<const T*>(a.lam) + head);
+        const float cs = kScaled ? f.scales[0] : 1.f;
+        const float lam = Elem<T>::one(static_cast<const T*>(a.lam) + head);
         float nl[2] = {-INFINITY, -INFINITY}, ne[2] = {0.f, 0.f};
         if (tok < a.Lq) {
             const float* r = a.rowv + attn_rowv(a, n, head, tok);
@@ -177,6 +181,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), al2 = make_float2(-lam, -lam);
         const float2 n0 = make_float2(nl[0], nl[0]), n1 = make_float2(nl[1], nl[1]);
         const float2 e0 = make_float2(ne[0], ne[0]), e1 = make_float2(ne[1], ne[1]);
+        // sums over the keys of P_s dP, cs-fold: e_s from weights that were not rounded
+        float2 es0 = make_float2(0.f, 0.f), es1 = es0;
         bool ok = true;
         Ring v(NS);
         for (int i = 0; i < count; ++i, v.next()) {
@@ -215,6 +221,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 const float2 g = make_float2(dp[2 * c], dp[2 * c + 1]);
                 p0 = make_float2(ex2(p0.x), ex2(p0.y));
                 p1 = make_float2(ex2(p1.x), ex2(p1.y));
+                es0 = __ffma2_rn(p0, g, es0);
+                es1 = __ffma2_rn(p1, g, es1);
                 p0 = __fmul2_rn(p0, __fadd2_rn(g, e0));
                 p1 = __fmul2_rn(p1, __ffma2_rn(g, al2, e1));
                 d0[c] = Elem<T>::pack2(p0.x, p0.y);
@@ -237,6 +245,21 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             ok = mbar_wait(&g_done[(count - 1) & 1], (uint32_t)(((count - 1) >> 1) & 1), f.flags);
         __syncwarp();
         tmem_fence_after();
+        // The saved outputs carry the rounding of the forward's weights; grad_k, grad_v and
+        // grad_lambda, computed after this kernel, take the sums found here instead.
+        esum[h * kAmRows + row] = make_float2(es0.x + es0.y, es1.x + es1.y);
+        named_barrier(1, 512);
+        if (h == 0 && tok < a.Lq && ok) {
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x += esum[k * kAmRows + row].x;
+                y += esum[k * kAmRows + row].y;
+            }
+            float* r = f.rowv + attn_rowv(a, n, head, tok);
+            r[2 * kRowvTile] = -x / cs;
+            r[3 * kRowvTile] = -y / cs;
+        }
         const float out_scale = a.scale / cs;
         T* dst = static_cast<T*>(a.gq) + (((long long)n * a.Lq + tok) * a.M + head) * 2 * a.D;
         for (int m = 0; m < 2; ++m)
@@ -440,7 +463,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const bool seen = key < len && !(a.mask && a.mask[(long long)n * a.Lk + key]);
         // tokens from this one on see the key
         const int from = !seen ? 0x7fffffff : a.causal ? key - len + a.Lq : 0;
-        const float cs = f.scales[0], cp = f.scales[1];
+        const float cs = kScaled ? f.scales[0] : 1.f, cp = kScaled ? f.scales[1] : 1.f;
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
         const float2 cp2 = make_float2(cp, cp), cs2 = make_float2(cs, cs);
         const float2 r2 = make_float2(cs / cp, cs / cp);
