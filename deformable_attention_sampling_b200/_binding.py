@@ -664,13 +664,17 @@ def dcnv4_fused(x, w_om, b_om=None, groups=4, kh=3, kw=3, pad=1, dil=1, out=None
 _HERE = contextlib.nullcontext()
 
 
-def _on_device(t):
-    """A context in which the tensor's device is the current one (launches and
-    the current stream belong to the current device)."""
+def _scope(t, stream):
+    """A context in which the tensor's device and the call's stream are current:
+    the launch goes there, and so does the memory that the call allocates (a
+    block of the current stream's may still be in use by what runs there)."""
     import torch
-    if t.get_device() == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(t.device)
+    device = t.get_device()
+    if stream is None:
+        return _HERE if device == torch.cuda.current_device() else torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
+    return torch.cuda.stream(stream)
 
 
 def _same_device(first, *rest):
@@ -728,13 +732,14 @@ def axial_rope(x, pos, freqs, axis_pairs, interleaved=False, inverse=False, out=
     import torch
     N, L, M, D, A, (image, row) = _rope_checks(x, pos, freqs, axis_pairs, inverse, interleaved)
     code = dtype_code(x)
-    if out is None:
-        out = torch.empty((N, L, M, D), dtype=x.dtype, device=x.device)
-    _require(out.shape == x.shape and out.dtype == x.dtype and out.device == x.device
-             and out.is_contiguous(), "out has the wrong shape, dtype, device or layout")
-    with _on_device(x):
+    _require(out is None or (out.shape == x.shape and out.dtype == x.dtype
+                             and out.device == x.device and out.is_contiguous()),
+             "out has the wrong shape, dtype, device or layout")
+    with _scope(x, stream):
+        if out is None:
+            out = torch.empty((N, L, M, D), dtype=x.dtype, device=x.device)
         axial_rope_forward(x, pos, freqs, out, axis_pairs, N, L, M, D, A, pos.shape[0], image, row,
-                           int(bool(interleaved)), int(bool(inverse)), code, stream)
+                           int(bool(interleaved)), int(bool(inverse)), code)
     return out
 
 
@@ -747,14 +752,14 @@ def axial_rope_grad(x, pos, freqs, axis_pairs, grad_out, interleaved=False, inve
              "grad_out has the wrong shape, dtype or layout")
     _same_device(x, grad_out)
     code = dtype_code(x)
-    gx = torch.empty((N, L, M, D), dtype=x.dtype, device=x.device)
-    gp = None
-    if need_pos:    # no images: the launch that would fill a shared pos' gradient does not run
-        gp = (torch.empty if N else torch.zeros)(pos.shape, dtype=pos.dtype, device=x.device)
-    with _on_device(x):
+    with _scope(x, stream):
+        gx = torch.empty((N, L, M, D), dtype=x.dtype, device=x.device)
+        gp = None
+        if need_pos:    # no images: the launch that would fill a shared pos' gradient does not run
+            gp = (torch.empty if N else torch.zeros)(pos.shape, dtype=pos.dtype, device=x.device)
         axial_rope_backward(x, pos, freqs, grad_out, gx, gp, axis_pairs, N, L, M, D, A,
                             pos.shape[0], image, row, int(bool(interleaved)), int(bool(inverse)),
-                            code, stream)
+                            code)
     return gx, gp
 
 
@@ -794,13 +799,14 @@ def norm_residual(x, y, scale=None, gate=None, post_weight=None, post_bias=None,
     N, L, C, flags, code = _norm_checks(
         (x, y), ((scale, False), (gate, True), (post_weight, False), (post_bias, False),
                  (pre_weight, False), (pre_bias, False)), norm, post, pre)
-    z = torch.empty_like(x) if out is None else out
-    _require(z.shape == x.shape and z.dtype == x.dtype and z.device == x.device
-             and z.is_contiguous(), "out has the wrong shape, dtype, device or layout")
-    h = torch.empty_like(x) if pre else None
-    with _on_device(x):
+    _require(out is None or (out.shape == x.shape and out.dtype == x.dtype
+                             and out.device == x.device and out.is_contiguous()),
+             "out has the wrong shape, dtype, device or layout")
+    with _scope(x, stream):
+        z = torch.empty_like(x) if out is None else out
+        h = torch.empty_like(x) if pre else None
         norm_residual_forward(x, y, scale, gate, post_weight, post_bias, pre_weight, pre_bias, z,
-                              h, N, L, C, flags, eps, code, stream)
+                              h, N, L, C, flags, eps, code)
     return z, h
 
 
@@ -820,17 +826,17 @@ def norm_residual_grad(y, z, grad_z, grad_h=None, scale=None, gate=None, post_we
     def like(f):
         return None if f is None else torch.empty_like(f)
 
-    gx, gy = torch.empty_like(y), torch.empty_like(y)
-    gs, gg, gpw, gpb = like(scale), like(gate), like(post_weight), like(post_bias)
-    gqw, gqb = like(pre_weight), like(pre_bias)
-    with _on_device(y):
+    with _scope(y, stream):
+        gx, gy = torch.empty_like(y), torch.empty_like(y)
+        gs, gg, gpw, gpb = like(scale), like(gate), like(post_weight), like(post_bias)
+        gqw, gqb = like(pre_weight), like(pre_bias)
         need = norm_residual_backward_workspace_size(N, L, C, 0 if gate is None else 1, code)
         if need < 0:
             raise DcnError(need, "norm_residual_backward_workspace_size")
         ws, ws_bytes = _workspace(need, y.device, workspace)
         norm_residual_backward(y, z, grad_z, grad_h, scale, gate, post_weight, post_bias,
                                pre_weight, gx, gy, gs, gg, gpw, gpb, gqw, gqb, ws, ws_bytes, N, L,
-                               C, flags, eps, code, stream)
+                               C, flags, eps, code)
     return gx, gy, gs, gg, gpw, gpb, gqw, gqb
 
 
@@ -869,23 +875,23 @@ def diff_attn(q, k, v, lam, mask=None, lengths=None, causal=False, scale=None, s
     import torch
     (N, Lq, Lk, M, Mk, D, Dv), strides = _attn_checks(q, k, v, lam, mask, lengths)
     code = dtype_code(q)
-    if out is None:
-        out = torch.empty((N, Lq, M, Dv), dtype=q.dtype, device=q.device)
-    _require(tuple(out.shape) == (N, Lq, M, Dv) and out.dtype == q.dtype
-             and out.device == q.device and out.is_contiguous(),
+    _require(out is None or (tuple(out.shape) == (N, Lq, M, Dv) and out.dtype == q.dtype
+                             and out.device == q.device and out.is_contiguous()),
              "out has the wrong shape, dtype, device or layout")
     maps = lse = None
-    if save:
-        maps = torch.empty((N, Lq, M, 2, Dv), dtype=torch.float32, device=q.device)
-        lse = torch.empty((N, M, 2, Lq), dtype=torch.float32, device=q.device)
-    with _on_device(q):
+    with _scope(q, stream):
+        if out is None:
+            out = torch.empty((N, Lq, M, Dv), dtype=q.dtype, device=q.device)
+        if save:
+            maps = torch.empty((N, Lq, M, 2, Dv), dtype=torch.float32, device=q.device)
+            lse = torch.empty((N, M, 2, Lq), dtype=torch.float32, device=q.device)
         need = diff_attn_forward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, code)
         if need < 0:
             raise DcnError(need, "diff_attn_forward_workspace_size")
         ws, ws_bytes = _workspace(need, q.device, workspace)
         diff_attn_forward(q, k, v, lam, mask, lengths, out, maps, lse, ws, ws_bytes, N, Lq, Lk, M,
                           Mk, D, Dv, *strides, D ** -0.5 if scale is None else scale,
-                          int(bool(causal)), code, stream)
+                          int(bool(causal)), code)
     return (out, (maps, lse)) if save else out
 
 
@@ -904,16 +910,16 @@ def diff_attn_grad(q, k, v, lam, out, saved, grad_out, mask=None, lengths=None, 
     for t, shape in ((maps, (N, Lq, M, 2, Dv)), (lse, (N, M, 2, Lq))):
         _require(tuple(t.shape) == shape and t.dtype == torch.float32 and t.is_contiguous(),
                  "saved must be diff_attn's")
-    gq = torch.empty((N, Lq, M, 2, D), dtype=q.dtype, device=q.device)
-    gk = torch.empty((N, Lk, Mk, 2, D), dtype=q.dtype, device=q.device)
-    gv = torch.empty((N, Lk, Mk, Dv), dtype=q.dtype, device=q.device)
-    gl = torch.empty_like(lam)
-    with _on_device(q):
+    with _scope(q, stream):
+        gq = torch.empty((N, Lq, M, 2, D), dtype=q.dtype, device=q.device)
+        gk = torch.empty((N, Lk, Mk, 2, D), dtype=q.dtype, device=q.device)
+        gv = torch.empty((N, Lk, Mk, Dv), dtype=q.dtype, device=q.device)
+        gl = torch.empty_like(lam)
         need = diff_attn_backward_workspace_size(N, Lq, Lk, M, Mk, D, Dv, code)
         if need < 0:
             raise DcnError(need, "diff_attn_backward_workspace_size")
         ws, ws_bytes = _workspace(need, q.device, workspace)
         diff_attn_backward(q, k, v, lam, mask, lengths, maps, lse, grad_out, gq, gk, gv, gl,
                            ws, ws_bytes, N, Lq, Lk, M, Mk, D, Dv, *strides,
-                           D ** -0.5 if scale is None else scale, int(bool(causal)), code, stream)
+                           D ** -0.5 if scale is None else scale, int(bool(causal)), code)
     return gq, gk, gv, gl

@@ -238,7 +238,7 @@ bool head_map(CUtensorMap* map, const void* p, int dtype, int inner, int heads, 
               long long row, long long image, int rows) {
     const uint64_t dims[4] = {(uint64_t)inner, (uint64_t)heads, (uint64_t)L, (uint64_t)N};
     const uint64_t strides[3] = {(uint64_t)inner * 2, (uint64_t)row * 2,
-                                 (uint64_t)(N == 1 ? row * L : image) * 2};
+                                 (uint64_t)(N == 1 ? row : image) * 2};   // (of one image: unused)
     const uint32_t box[4] = {64, 1, (uint32_t)rows, 1};
     return encode_tmap_4d(map, p, dtype == DCN_BF16, dims, strides, box);
 }

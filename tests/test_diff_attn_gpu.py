@@ -205,6 +205,14 @@ def test_other_streams_and_graphs():
         got = step()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # the stream as an argument, an object or a handle: launch and scratch go there
+    for stream in (side, side.cuda_stream):
+        side.wait_stream(torch.cuda.current_stream())
+        out, saved = dcnb.diff_attn(q, k, v, lam, causal=True, save=True, stream=stream)
+        got = (out, dcnb.diff_attn(q1, k, v, lam, causal=True, stream=stream)) + dcnb.diff_attn_grad(
+            q, k, v, lam, out, saved, go, causal=True, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
     graphs, outs = [], []
     for _ in range(2):
         g = torch.cuda.CUDAGraph()

@@ -213,3 +213,31 @@ def test_axial_rope_gradient_of_positions_against_differences():
     slope = (value(h) - value(-h)) / (2 * h)
     mag = float((gp.double().cpu() * d).abs().sum())
     assert abs(float((gp.double().cpu() * d).sum()) - slope) <= 1e-5 * mag + 1e-5
+
+
+def test_a_stream_as_an_argument():
+    x, pos, freqs, go = rope_inputs(2, 6, 3, 24, (5, 7), torch.bfloat16, 29)
+    (a, b, gz, gh), f = join_inputs(2, 7, 48, torch.bfloat16, 31, True, True, True, True)
+
+    def step(**kw):
+        z, h = dcnb.norm_residual(a, b, **f, **kw)
+        return ((dcnb.axial_rope(x, pos, freqs, (5, 7), **kw), z, h) +
+                dcnb.axial_rope_grad(x, pos, freqs, (5, 7), go, **kw) +
+                dcnb.norm_residual_grad(b, z, gz, gh, **f, **kw))
+
+    want = step()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        side.wait_stream(torch.cuda.current_stream())
+        got = step(stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_more_axes_than_tasks():
+    """One pair a token and four axes: the position gradients need as many lanes."""
+    x, pos, freqs, go = rope_inputs(3, 5, 1, 2, (0, 1, 0, 0), torch.float32, 33)
+    gx, gp = dcnb.axial_rope_grad(x, pos, freqs, (0, 1, 0, 0), go)
+    rx, rp = ref.rope(x, pos, freqs, (0, 1, 0, 0), False, False, go)
+    ref.check(gx, *rx, "grad_x")
+    ref.check(gp, *rp, "grad_pos")
