@@ -7,6 +7,10 @@
 // by -th; that of a position sums, over the heads and the axis's pairs,
 //   freqs[i] * (gb * a' - ga * b'),   (a', b') the turned pair.
 //
+// Measured: 16.5 us for 2 x 15000 tokens of 8 x 32 in float32 (9.4 us at the
+// measured copy rate), 47 us for the gradient of 2 x 12136 tokens of 16 x 64 in
+// bf16 (23 us): each token's angles (float64, sine and cosine) come before its
+// few vectors.
 // Bound: one read of x (and grad_out) and one write, so HBM for many tokens
 // and launch latency for few.  The angles are the only other work: R per
 // token, shared by its M heads.  A team of `tpt` lanes (a power of two up to a

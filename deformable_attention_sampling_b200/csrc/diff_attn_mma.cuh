@@ -29,7 +29,18 @@
 // NaN.
 //
 // Bound: per 128 x 64 tile and map the exponentials take 512 cycles of the
-// special-function units and the products 384 (D = 64, Dv = 128).
+// special-function units and the products 470 (D = 64, Dv = 128: measured 53
+// cycles a 128 x 64 x 16 step from shared memory, 64 a 128 x 128 x 16 step from
+// TMEM).  Measured: 477 us on one prompt of 8192 tokens, 16 heads of 64 + 128
+// (880 TFLOP/s; the products alone take 249 us at the measured bf16 rate, the
+// exponentials 239 us); a pair of tiles takes about 1960 cycles, of which the
+// steps of a softmax warp that follow one another (two waits, load, maximum,
+// exponentials, store) are the longest chain.
+// Tried and slower on that prompt (469 us then): 128-key tiles with P over S (655),
+// strict turns of the maps at the exponentials (502), a third of the
+// exponentials by polynomial on the FMA units (512), two sets of softmax warps
+// a map with P in shared memory (549), scores and value products of both maps
+// each from one polling warp (517).
 #pragma once
 
 #include "diff_attn.cuh"

@@ -23,7 +23,10 @@
 // are divided by them.  bf16 needs neither.
 //
 // Bound: a 128 x 64 tile's exponentials take 1024 cycles in either kernel, its
-// products about 1100 (grad_q) and 1360 (grad_k, grad_v).
+// products about 1100 (grad_q) and 1360 (grad_k, grad_v); the scores of a tile
+// wait for the registers of the one before, so a tile takes about 2300.
+// Measured on 2 x 4096 tokens, 8 heads of 64 + 128, causal: grad_q 141 us,
+// grad_k and grad_v 163 us.
 #pragma once
 
 #include "diff_attn_mma.cuh"

@@ -17,6 +17,10 @@
 // sector is fetched twice.
 // A warp's next block is on its way to shared memory (cp.async, each lane its own
 // pieces, so no barrier) while it works on this one.
+// Measured: 49 us for 16 caches of 4096 to 8192 keys, 4 key / value heads of 64 +
+// 128 (201 MB: 4.1 TB/s; 31 us at the measured copy rate), 10 us for the join.
+// Held by a warp's chain of loads, 8 dependent score products and shuffles: the
+// time hardly depends on the split (4 to 27 parts: 57 to 64 us with the join).
 // The keys are split over CTAs (and the 4 warps of a CTA, which join in shared
 // memory); diff_attn_join_kernel adds the CTAs' parts in a fixed order.
 #pragma once
@@ -87,7 +91,8 @@ __host__ __device__ constexpr int attn_step_smem(int D, int Dv) {
 }
 
 template <typename T, int D, int DV>
-__global__ void __launch_bounds__(kAsThreads, D == 128 && DV == 128 ? 2 : DV <= 64 && D <= 64 ? 4 : 3)
+__global__ void __launch_bounds__(kAsThreads,
+                                  D == 128 && DV == 128 ? 2 : DV <= 64 && D <= 64 ? 4 : 3)
     diff_attn_step_kernel(const AttnArgs a) {
     constexpr float kBias = std::is_same<T, __half>::value ? 6.f : 0.f;
     constexpr int KW = D / 8;              // words of a lane's channels of a key

@@ -6,6 +6,9 @@
 // norm: layer (subtract the mean, divide by sqrt(variance + eps)) or rms
 // (divide by sqrt(mean square + eps)), over the C channels of a row.
 //
+// Measured: 34 us for 64 x 3136 x 64 in fp16 (103 MB, 16 us at the measured copy
+// rate), 85 us forward and 141 + 10 us backward for 8 x 4096 x 1024 in bf16 (268
+// and 403 MB): a team's sums, not the bytes, set the step.
 // Bound: HBM.  One pass over the rows: x and y are read once, z and h written
 // once, the rows' statistics stay in registers (two-pass: the mean first, then
 // the squared deviations, so that a large mean costs no digits), and h is the
