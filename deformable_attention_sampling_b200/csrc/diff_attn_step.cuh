@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kAsThreads,
                              ((long long)head * 2 + m) * D + t * 8,
                          row < a.rows, q[m]);
     const T* kb = static_cast<const T*>(a.k) + n * a.k_image + (long long)kv * 2 * D + t * 8;
-    const T* vb = static_cast<const T*>(a.v) + n * a.v_image + (long long)kv * DV + g * (CPG < 8 ? CPG : 8);
+    const T* vb = static_cast<const T*>(a.v) + n * a.v_image + (long long)kv * DV +
+                  g * (CPG < 8 ? CPG : 8);
     const unsigned char* mask = a.mask ? a.mask + (long long)n * a.Lk : nullptr;
 
     float o[CPG][4], top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};

@@ -91,6 +91,17 @@ def test_steps_with_lengths(Lq, Lk, M, Mk, D, Dv, dt):
 
 
 @pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("N,Lq,Lk,M,Mk,D,Dv", [(1, 40, 700, 2, 1, 64, 256), (1, 20, 1500, 1, 1, 128, 128),
+                                               (2, 17, 900, 2, 2, 32, 64), (1, 130, 3000, 1, 1, 64, 64)])
+def test_few_tiles_over_many_keys(N, Lq, Lk, M, Mk, D, Dv, dt):
+    """Few query tiles: the keys are split, and some splits of a short image are empty."""
+    q, k, v, lam, go = inputs(N, Lq, Lk, M, Mk, D, Dv, DT[dt], 11)
+    run_and_check(q, k, v, lam, go)
+    lengths = torch.tensor([Lk // 3, 60][:N], dtype=torch.int32, device=DEV)
+    run_and_check(q, k, v, lam, go, lengths=lengths, causal=True)
+
+
+@pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("Lq,Lk,M,Mk,D,Dv", [(70, 150, 4, 2, 32, 64), (200, 300, 2, 1, 64, 128),
                                              (1, 260, 4, 4, 64, 64), (20, 40, 2, 2, 12, 20)])
 def test_masks(Lq, Lk, M, Mk, D, Dv, dt):
