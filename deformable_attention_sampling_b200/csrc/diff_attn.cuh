@@ -470,6 +470,19 @@ struct AttnDeltaArgs {
     int vec4;              // rows of the maps and of grad_out are aligned groups of 4
 };
 
+// at / d and at % d, in 32 bits where they suffice (a 64-bit division costs more
+// than the rest of a row).
+__device__ __forceinline__ void attn_split(long long at, int d, long long& q, int& r) {
+    if (at <= 0xffffffffLL) {
+        const uint32_t t = (uint32_t)at / (uint32_t)d;
+        q = t;
+        r = (int)((uint32_t)at - t * (uint32_t)d);
+    } else {
+        q = at / d;
+        r = (int)(at - q * d);
+    }
+}
+
 // One warp per (token, head), tokens padded to whole tiles: e_s = <g, O_s> from
 // the maps' own outputs, kept in float32 (with outputs rounded to 16 bits the
 // differences dP - e_s, and with them grad_q, grad_k and grad_lambda, carried
@@ -486,10 +499,14 @@ __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArg
     if ((int)blockIdx.x < d.g_blocks) {
         const int tiles = (a.Lq + kRowvTile - 1) / kRowvTile;
         const long long at = (long long)blockIdx.x * 8 + warp;
-        const long long tok_all = at / a.M;             // tokens of all images, padded
-        const int h = (int)(at - tok_all * a.M);
-        const int n = (int)(tok_all / (tiles * kRowvTile));
-        const int i = (int)(tok_all - (long long)n * tiles * kRowvTile);
+        long long tok_all;                              // tokens of all images, padded
+        int h, n, i;
+        attn_split(at, a.M, tok_all, h);
+        {
+            long long image;
+            attn_split(tok_all, tiles * kRowvTile, image, i);
+            n = (int)image;
+        }
         if (n < a.N) {
             float s = 0.f, s2 = 0.f, lse = INFINITY;
             if (i < a.Lq) {
@@ -520,9 +537,11 @@ __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArg
         }
     } else {
         const long long at = ((long long)blockIdx.x - d.g_blocks) * 8 + warp;
-        const long long key_all = at / a.Mk;
-        const int kv = (int)(at - key_all * a.Mk), n = (int)(key_all / a.Lk);
-        const int j = (int)(key_all - (long long)n * a.Lk);
+        long long key_all, image;
+        int kv, j;
+        attn_split(at, a.Mk, key_all, kv);
+        attn_split(key_all, a.Lk, image, j);
+        const int n = (int)image;
         if (n < a.N && j < attn_len(a, n) && !(a.mask && a.mask[(long long)n * a.Lk + j])) {
             const T* v = static_cast<const T*>(a.v) + n * a.v_image + (long long)j * a.v_row +
                          (long long)kv * a.Dv;
