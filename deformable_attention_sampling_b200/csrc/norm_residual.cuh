@@ -347,8 +347,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == kNormSmall ? 2 : 1)
                 q += zv[e] * zv[e];
             }
             const float2 s = sum(p, q);
-            r1 = a.post ? 1.0f / sqrtf(s.x * inv_c + a.eps) : 1.f;
-            r2 = 1.0f / sqrtf(s.y * inv_c + a.eps);
+            // (a team without a row has zeros here: with eps = 0 their spread is 0 too, and
+            // 0 / 0 would go into the column sums)
+            r1 = !a.post ? 1.f : live ? 1.0f / sqrtf(s.x * inv_c + a.eps) : 0.f;
+            r2 = live ? 1.0f / sqrtf(s.y * inv_c + a.eps) : 0.f;
         }
         if (a.pre) {
             float p = 0.f, q = 0.f;
