@@ -515,8 +515,9 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
         if ((rc = attn_pointers(a, es)) != DCN_OK) return rc;
         if (!maps || !lse || !grad_out || !grad_q || !workspace) return DCN_ERR_INVALID_ARG;
     }
-    if (keys > 0 && (!grad_k || !grad_v)) return DCN_ERR_INVALID_ARG;
-    if (((uintptr_t)grad_out | (uintptr_t)grad_q |
+    // the key kernel reads k and v whether or not there are tokens
+    if (keys > 0 && (!k || !v || !grad_k || !grad_v)) return DCN_ERR_INVALID_ARG;
+    if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)grad_out | (uintptr_t)grad_q |
          (uintptr_t)grad_k | (uintptr_t)grad_v | (uintptr_t)grad_lambda) % es != 0 ||
         ((uintptr_t)lse | (uintptr_t)maps | (uintptr_t)lengths) % 4 != 0 || (uintptr_t)workspace % 16 != 0)
         return DCN_ERR_MISALIGNED;
