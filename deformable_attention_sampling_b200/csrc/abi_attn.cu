@@ -308,14 +308,15 @@ long long rowv_floats(int N, int Lq, int M) {
 
 // Row values (and fp16's scales) are set; `glam` sums grad_lambda from the row
 // values between the two kernels: the first one refines them.
-int mma_backward(const dcnb::AttnArgs& a, const float* scales, float* rowv, const void* glam,
-                 const dcnb::AttnDeltaArgs& d, int dtype, void* stream) {
+int mma_backward(const dcnb::AttnArgs& a, const void* glam, const dcnb::AttnDeltaArgs& d,
+                 int dtype, void* stream) {
     dcnb::AttnBwdArgs f;
-    f.rowv = rowv;
+    f.rowv = d.rowv;
     f.a = a;
     f.negate = a.scale < 0.f ? 1 : 0;
     f.a.scale_log2 = std::max(std::fabs(a.scale_log2), 1e-30f);
-    f.scales = scales;
+    f.scales = d.scales;
+    f.gnorm = d.gnorm;
     f.flags = device_flags_word();
     f.dsteps = ceil_div(a.D, 16);
     f.vsteps = ceil_div(a.Dv, 16);
@@ -489,10 +490,11 @@ long long diff_attn_backward_workspace_size(int N, int Lq, int Lk, int M, int Mk
     const int st = attn_setup(&a, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, N, Lq, Lk,
                               M, Mk, D, Dv, 0, qd, 0, kd, 0, vd, 1.f, 0, dtype);
     if (st != DCN_OK) return st;
-    // row values, the two scales (16 bytes), the blocks' peaks of the scaled fp16 kernels
-    long long floats = rowv_floats(N, Lq, M) + 4;
+    // row values; of the scaled fp16 kernels the scales (16 bytes each), the rows' |g|^2 (one
+    // where the row values have four) and the keys' |v|^2
+    long long floats = rowv_floats(N, Lq, M);
     if (dtype == DCN_F16 && mma_bwd_sizes(dtype, Lq, Lk, D, Dv))
-        floats += rowv_floats(N, Lq, M) / 32 + ((long long)N * Lk * Mk + 7) / 8;
+        floats += 4LL * N * Mk + rowv_floats(N, Lq, M) / 4 + (long long)N * Lk * Mk;
     return floats * 4;
 }
 
@@ -573,7 +575,6 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
     d.lam = lambda;
     d.lse = lse;
     d.rowv = ws;
-    d.scales = ws + rowv_floats(N, Lq, M);
     d.glam = grad_lambda;
     d.vec4 = Dv % 4 == 0 && (uintptr_t)maps % 16 == 0 &&
              (uintptr_t)grad_out % (uintptr_t)(4 * es) == 0;
@@ -582,19 +583,22 @@ int diff_attn_backward(const void* q, const void* k, const void* v, const void* 
     if (g_blocks + v_blocks > kInt31) return DCN_ERR_UNSUPPORTED;
     d.g_blocks = (int)g_blocks;
     d.v_blocks = (int)v_blocks;
-    if (v_blocks > 0) d.peak = d.scales + 4;
+    if (v_blocks > 0) {
+        d.scales = reinterpret_cast<float4*>(ws + rowv_floats(N, Lq, M));
+        d.gnorm = ws + rowv_floats(N, Lq, M) + 4LL * N * Mk;
+        d.vnorm = d.gnorm + rowv_floats(N, Lq, M) / 4;
+    }
     if (tokens > 0) {
         rc = launch_grid(delta, d, (int)(g_blocks + v_blocks), 256, 0, stream);
         if (rc != DCN_OK) return rc;
     }
     if (mma) {
-        if (d.peak) {
-            dcnb::AttnDeltaArgs scales = d;
-            scales.first_block = M;
-            rc = launch_grid(glam, scales, 1, 1024, 0, stream);
+        if (d.scales) {
+            rc = launch_grid((const void*)dcnb::diff_attn_scales_kernel<__half>, d, N * Mk, 1024, 0,
+                             stream);
             if (rc != DCN_OK) return rc;
         }
-        return mma_backward(a, d.scales, ws, glam, d, dtype, stream);
+        return mma_backward(a, glam, d, dtype, stream);
     }
     rc = launch_grid(glam, d, M, 1024, 0, stream);       // zeros for an empty batch
     if (rc != DCN_OK) return rc;

@@ -82,6 +82,12 @@ __device__ __forceinline__ long long attn_rowv(const AttnArgs& a, int n, int hea
            tok % kRowvTile;
 }
 
+// Place of token tok's |g|^2: tokens of a head side by side, padded to whole tiles.
+__device__ __forceinline__ long long attn_gnorm(const AttnArgs& a, int n, int head, int tok) {
+    const int tiles = (a.Lq + kRowvTile - 1) / kRowvTile;
+    return (((long long)n * a.M + head) * tiles) * kRowvTile + tok;
+}
+
 // Four elements of a row at column d (D in all) as float32, zeros past the end.
 template <typename T>
 __device__ __forceinline__ float4 attn_ld4(const T* row, int d, int D, int vec4) {
@@ -458,15 +464,15 @@ __global__ void __launch_bounds__(kJoinThreads) diff_attn_join_kernel(const Attn
 struct AttnDeltaArgs {
     const float* maps;
     const void* go;
-    const void* lam;       // second kernel
+    const void* lam;       // scales kernel
     const float* lse;
     AttnArgs a;            // geometry, visible keys and v
     float* rowv;
-    void* glam;            // second kernel
-    float* peak;           // [blocks] largest |g|^2 and |v|^2 of a block, or null
-    float* scales;         // cs, cp
+    void* glam;            // grad_lambda kernel
+    float* gnorm;          // [N][M][tiles * 64] |g|^2 of a row, or null
+    float* vnorm;          // [N][Mk][Lk] |v|^2 of a visible key (0 of a hidden one), or null
+    float4* scales;        // [N][Mk] cs and cp of the key kernel, the largest |v|
     int g_blocks, v_blocks;
-    int first_block;       // of the second kernel: its blocks count from here
     int vec4;              // rows of the maps and of grad_out are aligned groups of 4
 };
 
@@ -488,14 +494,12 @@ __device__ __forceinline__ void attn_split(long long at, int d, long long& q, in
 // differences dP - e_s, and with them grad_q, grad_k and grad_lambda, carried
 // that rounding: grad_lambda was off by up to twice a 16-bit result's own).
 // Rows past the end and rows that see no key get -lse = -inf: weights of 0.
-// With `peak` the blocks also find the largest |g|^2 and, in blocks of their
-// own, the largest |v|^2 of a visible key.
+// With `gnorm` and `vnorm` also |g|^2 of every row and, in blocks of their own,
+// |v|^2 of every key.
 template <typename T>
 __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArgs d) {
-    __shared__ float top[8];
     const AttnArgs& a = d.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float peak = 0.f;
     if ((int)blockIdx.x < d.g_blocks) {
         const int tiles = (a.Lq + kRowvTile - 1) / kRowvTile;
         const long long at = (long long)blockIdx.x * 8 + warp;
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArg
             n = (int)image;
         }
         if (n < a.N) {
-            float s = 0.f, s2 = 0.f, lse = INFINITY;
+            float s = 0.f, s2 = 0.f, norm = 0.f, lse = INFINITY;
             if (i < a.Lq) {
                 const long long row = (((long long)n * a.Lq + i) * a.M + h) * a.Dv;
                 const T* g = static_cast<const T*>(d.go) + row;
@@ -520,20 +524,21 @@ __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArg
                     const float4 o2v = attn_ld4<float>(o + a.Dv, c, a.Dv, d.vec4);
                     s = dot4(s, gv, ov);
                     s2 = dot4(s2, gv, o2v);
-                    peak = dot4(peak, gv, gv);
+                    norm = dot4(norm, gv, gv);
                 }
                 if (lane < 2) lse = d.lse[(((long long)n * a.M + h) * 2 + lane) * a.Lq + i];
             }
             for (int w = 16; w > 0; w >>= 1) {
                 s += __shfl_xor_sync(0xffffffffu, s, w);
                 s2 += __shfl_xor_sync(0xffffffffu, s2, w);
-                peak += __shfl_xor_sync(0xffffffffu, peak, w);
+                norm += __shfl_xor_sync(0xffffffffu, norm, w);
             }
             float* r = d.rowv + attn_rowv(a, n, h, i);
             if (lane < 2) {
                 r[lane * kRowvTile] = -lse;
                 r[(2 + lane) * kRowvTile] = lane ? -s2 : -s;
             }
+            if (d.gnorm && lane == 0) d.gnorm[attn_gnorm(a, n, h, i)] = norm;
         }
     } else {
         const long long at = ((long long)blockIdx.x - d.g_blocks) * 8 + warp;
@@ -542,23 +547,18 @@ __global__ void __launch_bounds__(256) diff_attn_delta_kernel(const AttnDeltaArg
         attn_split(at, a.Mk, key_all, kv);
         attn_split(key_all, a.Lk, image, j);
         const int n = (int)image;
-        if (n < a.N && j < attn_len(a, n) && !(a.mask && a.mask[(long long)n * a.Lk + j])) {
+        if (n >= a.N) return;
+        float norm = 0.f;
+        if (j < attn_len(a, n) && !(a.mask && a.mask[(long long)n * a.Lk + j])) {
             const T* v = static_cast<const T*>(a.v) + n * a.v_image + (long long)j * a.v_row +
                          (long long)kv * a.Dv;
             for (int c = lane; c < a.Dv; c += 32) {
                 const float x = Elem<T>::one(v + c);
-                peak = fmaf(x, x, peak);
+                norm = fmaf(x, x, norm);
             }
         }
-        for (int w = 16; w > 0; w >>= 1) peak += __shfl_xor_sync(0xffffffffu, peak, w);
-    }
-    if (d.peak) {
-        if (lane == 0) top[warp] = peak;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < 8; ++w) peak = fmaxf(peak, top[w]);
-            d.peak[blockIdx.x] = peak;
-        }
+        for (int w = 16; w > 0; w >>= 1) norm += __shfl_xor_sync(0xffffffffu, norm, w);
+        if (lane == 0) d.vnorm[((long long)n * a.Mk + kv) * a.Lk + j] = norm;
     }
 }
 
@@ -569,51 +569,62 @@ __device__ __forceinline__ float attn_pow2(float x) {
     return exp2f(fminf(fmaxf(15.f - ceilf(log2f(x)), -40.f), 40.f));
 }
 
-// Block h: grad_lambda of head h, in a fixed order.  Block M sets the scales of
-// the tensor-core kernels' fp16 operands from the delta kernel's peaks.
+// The power of two for the score gradients of a row or of several:
+// |dS| <= 2 max(1, |lambda|) |g| |v| with the largest of each among them.
+__device__ __forceinline__ float attn_grad_scale(float lam, float g, float v) {
+    return attn_pow2(2.f * fmaxf(1.f, fabsf(lam)) * g * v);
+}
+
+// Block (n, a): the scales of the key kernel's fp16 operands, from the rows of
+// image n and the heads of key / value head a, and the largest |v| of its keys.
 template <typename T>
-__global__ void __launch_bounds__(1024) diff_attn_glam_kernel(const AttnDeltaArgs d) {
+__global__ void __launch_bounds__(1024) diff_attn_scales_kernel(const AttnDeltaArgs d) {
     __shared__ float part[32][3];
     const AttnArgs& a = d.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if ((int)blockIdx.x + d.first_block == a.M) {
-        float x[3] = {0.f, 0.f, 0.f};
-        {
-            for (int i = threadIdx.x; i < d.g_blocks + d.v_blocks; i += 1024) {
-                const int k = i < d.g_blocks ? 0 : 1;
-                x[k] = fmaxf(x[k], d.peak[i]);
-            }
-            for (int h = threadIdx.x; h < a.M; h += 1024)
-                x[2] = fmaxf(x[2], fabsf(Elem<T>::one(static_cast<const T*>(d.lam) + h)));
-        }
+    const int n = (int)a.div_Mk.div(blockIdx.x), kv = (int)blockIdx.x - n * a.Mk;
+    float x[3] = {0.f, 0.f, 0.f};
+    // the rows of a group's heads follow one another
+    const float* g = d.gnorm + attn_gnorm(a, n, kv * a.G, 0);
+    const long long rows = attn_gnorm(a, 0, a.G, 0);
+    for (long long i = threadIdx.x; i < rows; i += 1024) x[0] = fmaxf(x[0], g[i]);
+    const float* v = d.vnorm + (long long)blockIdx.x * a.Lk;
+    for (int i = threadIdx.x; i < a.Lk; i += 1024) x[1] = fmaxf(x[1], v[i]);
+    for (int h = threadIdx.x; h < a.G; h += 1024)
+        x[2] = fmaxf(x[2], fabsf(Elem<T>::one(static_cast<const T*>(d.lam) + kv * a.G + h)));
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            for (int w = 16; w > 0; w >>= 1)
-                x[k] = fmaxf(x[k], __shfl_xor_sync(0xffffffffu, x[k], w));
-            if (lane == 0) part[warp][k] = x[k];
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < 32; ++w)
-                for (int k = 0; k < 3; ++k) part[0][k] = fmaxf(part[0][k], part[w][k]);
-            const float lam = part[0][2];
-            // |dS| <= 2 max(1, |lambda|) |g| |v|, |P_0 - lambda P_1| <= 1 + |lambda|
-            d.scales[0] = attn_pow2(2.f * fmaxf(1.f, lam) * sqrtf(part[0][0]) *
-                                    sqrtf(part[0][1]));
-            d.scales[1] = attn_pow2(1.f + lam);
-        }
-        return;
+    for (int k = 0; k < 3; ++k) {
+        for (int w = 16; w > 0; w >>= 1)
+            x[k] = fmaxf(x[k], __shfl_xor_sync(0xffffffffu, x[k], w));
+        if (lane == 0) part[warp][k] = x[k];
     }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 32; ++w)
+            for (int k = 0; k < 3; ++k) part[0][k] = fmaxf(part[0][k], part[w][k]);
+        const float lam = part[0][2], most = sqrtf(part[0][1]);
+        // |P_0 - lambda P_1| <= 1 + |lambda|
+        d.scales[blockIdx.x] = make_float4(attn_grad_scale(lam, sqrtf(part[0][0]), most),
+                                           attn_pow2(1.f + lam), most, 0.f);
+    }
+}
+
+// Block h: grad_lambda of head h, in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(1024) diff_attn_glam_kernel(const AttnDeltaArgs d) {
+    __shared__ float part[32];
+    const AttnArgs& a = d.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x;
     float s = 0.f;
     for (int n = 0; n < a.N; ++n)
         for (int i = threadIdx.x; i < a.Lq; i += 1024)
             s += d.rowv[attn_rowv(a, n, h, i) + 3 * kRowvTile];
     for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    if (lane == 0) part[warp][0] = s;
+    if (lane == 0) part[warp] = s;
     __syncthreads();
     if (threadIdx.x < 32) {
-        s = part[threadIdx.x][0];
+        s = part[threadIdx.x];
         for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
         if (threadIdx.x == 0) static_cast<T*>(d.glam)[h] = Elem<T>::from(s);
     }

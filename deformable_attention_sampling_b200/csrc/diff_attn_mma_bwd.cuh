@@ -17,10 +17,15 @@
 // of keys no token may see (0 times NaN).  The left operands are 16-bit, in
 // TMEM (dS) and shared memory (P_0 - lambda P_1).
 //
-// fp16 operands are scaled by powers of two: dS by cs with |dS| cs <= 2^15 for
-// the largest |g|, |v| and |lambda| of the call (incoming gradients may be of
-// any size), the weights by cp with |P_0 - lambda P_1| cp <= 2^15; the results
-// are divided by them.  bf16 needs neither.
+// fp16 operands are scaled by powers of two: dS by cs with |dS| cs <= 2^15
+// (incoming gradients may be of any size), the weights by cp with
+// |P_0 - lambda P_1| cp <= 2^15; the results are divided by them.  The query
+// kernel's cs is a row's own, from its |g| and lambda and the largest |v| of its
+// keys; the key kernel sums over tokens and takes one of an image and key / value
+// head, from the largest |g| and |lambda| among them.  So no image, no group of
+// heads and, in grad_q, no token loses digits to a larger one beside it; in grad_k
+// a dS 2^28 times below the largest that its image and group could have does (fp16
+// is subnormal there).  bf16 needs neither.
 //
 // Bound: a 128 x 64 tile's exponentials take 1024 cycles in either kernel, its
 // products about 1100 (grad_q) and 1360 (grad_k, grad_v); the scores of a tile
@@ -44,7 +49,8 @@ struct AttnBwdArgs {
     CUtensorMap tv;            // [N][Lk][Mk][Dv]
     CUtensorMap tg;            // [N][Lq][M][Dv]
     AttnArgs a;
-    const float* scales;       // cs, cp (fp16)
+    const float4* scales;      // [N][Mk] cs, cp, largest |v| (fp16)
+    const float* gnorm;        // |g|^2 of the rows (fp16)
     float* rowv;               // the row values, whose e_s the first kernel rewrites
     unsigned int* flags;
     int dsteps, vsteps;        // K = 16 steps of a head, of the values
@@ -170,8 +176,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const int row = quarter * 32 + lane, tok = q0 + row;
         const uint32_t t_row = tmem + ((uint32_t)(quarter * 32) << 16);
         const int limit = a.causal ? min(len, tok + len - a.Lq + 1) : len;
-        const float cs = kScaled ? f.scales[0] : 1.f;
         const float lam = Elem<T>::one(static_cast<const T*>(a.lam) + head);
+        const float cs = kScaled && tok < a.Lq
+                             ? attn_grad_scale(lam, sqrtf(f.gnorm[attn_gnorm(a, n, head, tok)]),
+                                               f.scales[n * a.Mk + kv].z)
+                             : 1.f;
         float nl[2] = {-INFINITY, -INFINITY}, ne[2] = {0.f, 0.f};
         if (tok < a.Lq) {
             const float* r = a.rowv + attn_rowv(a, n, head, tok);
@@ -466,7 +475,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const bool seen = key < len && !(a.mask && a.mask[(long long)n * a.Lk + key]);
         // tokens from this one on see the key
         const int from = !seen ? 0x7fffffff : a.causal ? key - len + a.Lq : 0;
-        const float cs = kScaled ? f.scales[0] : 1.f, cp = kScaled ? f.scales[1] : 1.f;
+        const float4 scales = kScaled ? f.scales[nk] : make_float4(1.f, 1.f, 0.f, 0.f);
+        const float cs = scales.x, cp = scales.y;
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
         const float2 cp2 = make_float2(cp, cp), cs2 = make_float2(cs, cs);
         const float2 r2 = make_float2(cs / cp, cs / cp);
