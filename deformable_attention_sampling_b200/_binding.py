@@ -515,6 +515,7 @@ def _workspace(nbytes, device, workspace):
     if workspace is None:
         workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=device)
     _require(workspace.is_cuda and workspace.is_contiguous(), "workspace must be a CUDA tensor")
+    _require(workspace.device == device, "workspace must be on the tensors' device")
     have = workspace.numel() * workspace.element_size()
     _require(have >= nbytes, f"workspace holds {have} bytes, {nbytes} needed")
     return workspace, have
@@ -674,6 +675,7 @@ def _scope(t, stream):
         return _HERE if device == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream), device=t.device)
+    _require(stream.device == t.device, "the stream must be one of the tensors' device")
     return torch.cuda.stream(stream)
 
 
