@@ -705,7 +705,7 @@ def _heads_stride(t, shape, name):
     return (image, row) if N * L else (L * inner, inner)
 
 
-def _rope_checks(x, pos, freqs, axis_pairs, inverse, interleaved):
+def _rope_checks(x, pos, freqs, axis_pairs):
     import torch
     _require(x.dim() == 4 and pos.dim() == 3, "expected x [N,L,M,D], pos [N or 1,L,A]")
     N, L, M, D = x.shape
@@ -732,7 +732,7 @@ def axial_rope(x, pos, freqs, axis_pairs, interleaved=False, inverse=False, out=
     the number of channel pairs each axis turns.  `out` may be x (in place).
     """
     import torch
-    N, L, M, D, A, (image, row) = _rope_checks(x, pos, freqs, axis_pairs, inverse, interleaved)
+    N, L, M, D, A, (image, row) = _rope_checks(x, pos, freqs, axis_pairs)
     code = dtype_code(x)
     _require(out is None or (out.shape == x.shape and out.dtype == x.dtype
                              and out.device == x.device and out.is_contiguous()),
@@ -749,7 +749,7 @@ def axial_rope_grad(x, pos, freqs, axis_pairs, grad_out, interleaved=False, inve
                     need_pos=True, stream=None):
     """axial_rope_backward: returns (grad_x, grad_pos); grad_pos is None without need_pos."""
     import torch
-    N, L, M, D, A, (image, row) = _rope_checks(x, pos, freqs, axis_pairs, inverse, interleaved)
+    N, L, M, D, A, (image, row) = _rope_checks(x, pos, freqs, axis_pairs)
     _require(grad_out.shape == x.shape and grad_out.dtype == x.dtype and grad_out.is_contiguous(),
              "grad_out has the wrong shape, dtype or layout")
     _same_device(x, grad_out)
@@ -900,13 +900,15 @@ def diff_attn(q, k, v, lam, mask=None, lengths=None, causal=False, scale=None, s
 def diff_attn_grad(q, k, v, lam, out, saved, grad_out, mask=None, lengths=None, causal=False,
                    scale=None, workspace=None, stream=None):
     """diff_attn_backward: returns (grad_q, grad_k, grad_v, grad_lam), dense;
-    out, saved: what diff_attn(..., save=True) returned for these inputs."""
+    saved: the second of what diff_attn(..., save=True) returned for these
+    inputs.  out, the first, is not read (the maps' own outputs in `saved` are):
+    it may be None, and need not be kept."""
     import torch
     (N, Lq, Lk, M, Mk, D, Dv), strides = _attn_checks(q, k, v, lam, mask, lengths)
     code = dtype_code(q)
     maps, lse = saved
     _same_device(q, out, maps, lse, grad_out)
-    for t in (out, grad_out):
+    for t in (grad_out,) if out is None else (out, grad_out):
         _require(tuple(t.shape) == (N, Lq, M, Dv) and t.dtype == q.dtype and t.is_contiguous(),
                  "out and grad_out must be contiguous [N, Lq, M, Dv] of q's dtype")
     for t, shape in ((maps, (N, Lq, M, 2, Dv)), (lse, (N, M, 2, Lq))):

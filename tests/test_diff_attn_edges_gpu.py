@@ -67,3 +67,12 @@ def test_token_first_and_broadcast_inputs(dt, Lq, D, Dv):
 
     run_and_check(token_first(q), token_first(k), token_first(v), lam, go, **kw)
     run_and_check(q, k[:1].expand(k.shape), v[:1].expand(v.shape), lam, go, **kw)
+
+
+def test_gradients_without_the_output():
+    """The gradient needs what was saved, not `out`: a caller may let it go."""
+    q, k, v, lam, go = inputs(2, 40, 50, 4, 2, 64, 64, torch.bfloat16, 24)
+    out, saved = dcnb.diff_attn(q, k, v, lam, save=True)
+    for a, b in zip(dcnb.diff_attn_grad(q, k, v, lam, None, saved, go),
+                    dcnb.diff_attn_grad(q, k, v, lam, out, saved, go)):
+        assert torch.equal(a, b)
