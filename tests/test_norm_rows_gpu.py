@@ -33,3 +33,13 @@ def run_and_check(shape, dtype, norm, gate, bias, eps):
 def test_no_eps(N, L, C, gate, norm, dt, eps):
     """eps = 0 (or 0 in float32): a team without a row must not add 0 / 0 to the sums."""
     run_and_check((N, L, C), DT[dt], norm, gate, True, eps)
+
+
+@pytest.mark.parametrize("dt,norm,bias", [("f32", "layer", True), ("bf16", "rms", False)])
+@pytest.mark.parametrize("N,L,C,gate", [(1, 2501, 1024, False), (3, 1203, 1000, True),
+                                        (1, 1001, 4096, False), (2, 388, 8192, True),
+                                        (1, 20011, 64, False)])
+def test_several_steps_a_block(N, L, C, gate, dt, norm, bias):
+    """Blocks walk several rows and end in a step that not every team takes part in:
+    prefetched rows, the second row of a team, column sums over steps."""
+    run_and_check((N, L, C), DT[dt], norm, gate, bias, 1e-5)
