@@ -27,11 +27,11 @@ NormShape norm_shape(int es, long long rows, int C) {
     return s;
 }
 
-// Blocks that share an image's rows in the gradient: two blocks a
-// multiprocessor (its registers hold no more) over all images (more only adds partial rows to sum), at
-// least one team step each.
+// Blocks that share an image's rows in the gradient: over all images as many as
+// a multiprocessor's registers hold, two of 256 threads or one of 512 or 1024
+// (more would only add partial rows to sum), at least one team step each.
 int grad_blocks_per_image(long long images, long long rows_per_image, int teams, int threads) {
-    const long long wanted = std::max(2LL * sm_count() * kNormBlockThreads / threads, 1LL);
+    const long long wanted = (threads <= dcnb::kNormSmall ? 2LL : 1LL) * sm_count();
     long long per = wanted / images;
     per = std::min(per, (rows_per_image + teams - 1) / teams);
     return (int)std::max(per, 1LL);

@@ -56,3 +56,12 @@ def test_a_workspace_of_another_device_is_refused():
     assert _binding._workspace(64, device, _OnDevice(0))[1] == 64
     with pytest.raises(ValueError):
         _binding._workspace(64, device, _OnDevice(1))
+
+
+def test_join_gradient_blocks_of_long_rows(lib):  # noqa: F811
+    """A block of 512 threads (up to 4096 channels) or of 1024 (up to 8192) fills a
+    multiprocessor by its registers: both lengths have one partial row of each."""
+    def blocks(C):
+        return dcnb.norm_residual_backward_workspace_size(1, 100000, C, 0, 2) // (16 * C)
+
+    assert blocks(8192) == blocks(4096) and blocks(1024) == 2 * blocks(4096)
