@@ -17,6 +17,16 @@
 // of keys no token may see (0 times NaN).  The left operands are 16-bit, in
 // TMEM (dS) and shared memory (P_0 - lambda P_1).
 //
+// Roundings.  For grad_q a dS is the sum of two 16-bit parts, its rounding and
+// what that left over, each in a product of its own: one part alone added as much
+// error as the rounding of the result does (root mean square 1.5 times a single
+// rounding, now 1.03; the second part costs 25 us of 141 on the case below).
+// grad_k and grad_v keep one part: their operands share TMEM with two more
+// accumulators, and 1.4 times a single rounding is what they have.  The row sums
+// e_s in grad_q come from the forward's outputs, whose weights were rounded: a
+// quarter of a rounding, as the keys' errors average out.  grad_k, grad_v and
+// grad_lambda take sums of unrounded weights that the query kernel finds on its way.
+//
 // fp16 operands are scaled by powers of two: dS by cs with |dS| cs <= 2^15
 // (incoming gradients may be of any size), the weights by cp with
 // |P_0 - lambda P_1| cp <= 2^15; the results are divided by them.  The query
@@ -28,10 +38,11 @@
 // is subnormal there).  bf16 needs neither.
 //
 // Bound: a 128 x 64 tile's exponentials take 1024 cycles in either kernel, its
-// products about 1100 (grad_q) and 1360 (grad_k, grad_v); the scores of a tile
-// wait for the registers of the one before, so a tile takes about 2300.
-// Measured on 2 x 4096 tokens, 8 heads of 64 + 128, causal: grad_q 141 us,
-// grad_k and grad_v 163 us.
+// products about 1360; the scores of a tile wait for the registers of the one
+// before, so a tile takes about 2700 (grad_q: 16 more conversions and stores a
+// thread for the second parts) and 2300.
+// Measured on 2 x 4096 tokens, 8 heads of 64 + 128, causal: grad_q 166 us,
+// grad_k and grad_v 158 us.
 #pragma once
 
 #include "diff_attn_mma.cuh"
@@ -106,6 +117,13 @@ __device__ __forceinline__ void zero_hidden_rows(unsigned char* tile, int chunk_
     }
 }
 
+// What the rounding of x to the packed pair `w` left over, rounded itself.
+template <typename T>
+__device__ __forceinline__ uint32_t rest_of(float2 x, uint32_t w) {
+    x = __ffma2_rn(make_float2(Elem<T>::lo(w), Elem<T>::hi(w)), make_float2(-1.f, -1.f), x);
+    return Elem<T>::pack2(x.x, x.y);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kAbThreads, 1)
     diff_attn_dq_mma_kernel(const __grid_constant__ AttnBwdArgs f) {
@@ -136,9 +154,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     uint64_t* kv_clean = kv_empty + NS;
     uint64_t* s_full = kv_clean + NS;
     uint64_t* s_free = s_full + 1;
-    uint64_t* p_full = s_free + 1;        // [2]
-    uint64_t* g_done = p_full + 2;        // [2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g_done + 2);
+    uint64_t* p_full = s_free + 1;
+    uint64_t* g_done = p_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g_done + 1);
     uint32_t* vis = tmem_slot + 4;        // [NS][2]
     float2* esum = reinterpret_cast<float2*>(vis + 2 * NS);       // [4][128]
 
@@ -151,10 +169,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         }
         mbar_init(s_full, 1);
         mbar_init(s_free, 16);
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&p_full[b], 16);
-            mbar_init(&g_done[b], 1);
-        }
+        mbar_init(p_full, 16);
+        mbar_init(g_done, 1);
         mbar_fence_init();
     }
     if (warp == 17) {
@@ -166,7 +182,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // TMEM columns: scores 0, 64; dP 128; dS [2 buffers][2 maps] 32 each from 192;
+    // TMEM columns: scores 0, 64; dP 128; dS [high, low part][2 maps] 32 each from 192;
     // grad_q 64 a map from 320
     const uint32_t d_hi = (uint32_t)(umma_desc128(0, 0) >> 32), lo_k = 16u >> 4 << 16;
 
@@ -198,7 +214,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         bool ok = true;
         Ring v(NS);
         for (int i = 0; i < count; ++i, v.next()) {
-            const int b = i & 1, j0 = i * kAmKeys + 16 * h;
+            const int j0 = i * kAmKeys + 16 * h;
             if (a.mask) ok = mbar_wait(&kv_full[v.st], v.phase, f.flags);
             ok = ok && mbar_wait(s_full, (uint32_t)(i & 1), f.flags);
             ok = __all_sync(0xffffffffu, ok);
@@ -225,7 +241,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     s1[c] = bits >> c & 1 ? s1[c] : -INFINITY;
                 }
             }
-            uint32_t d0[8], d1[8];
+            uint32_t d0[8], d1[8], l0[8], l1[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 float2 p0 = __ffma2_rn(make_float2(s0[2 * c], s0[2 * c + 1]), sc2, n0);
@@ -239,22 +255,24 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 p1 = __fmul2_rn(p1, __ffma2_rn(g, al2, e1));
                 d0[c] = Elem<T>::pack2(p0.x, p0.y);
                 d1[c] = Elem<T>::pack2(p1.x, p1.y);
+                l0[c] = rest_of<T>(p0, d0[c]);
+                l1[c] = rest_of<T>(p1, d1[c]);
             }
-            // the products that read this buffer are done
-            if (i >= 2) ok = mbar_wait(&g_done[b], (uint32_t)(((i >> 1) - 1) & 1), f.flags);
+            // the products that read the operands of the last tile are done
+            if (i > 0) ok = mbar_wait(g_done, (uint32_t)((i - 1) & 1), f.flags);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tmem_fence_after();
-            tmem_st8(t_row + 192 + 64 * b + 8 * h, d0);
-            tmem_st8(t_row + 192 + 64 * b + 32 + 8 * h, d1);
+            tmem_st8(t_row + 192 + 8 * h, d0);
+            tmem_st8(t_row + 224 + 8 * h, d1);
+            tmem_st8(t_row + 256 + 8 * h, l0);
+            tmem_st8(t_row + 288 + 8 * h, l1);
             tmem_wait_st();
             tmem_fence_before();
             __syncwarp();
-            mbar_arrive_if(lane == 0, &p_full[b]);
+            mbar_arrive_if(lane == 0, p_full);
         }
-        // (the product before the last was waited for above)
-        if (ok && count > 0)
-            ok = mbar_wait(&g_done[(count - 1) & 1], (uint32_t)(((count - 1) >> 1) & 1), f.flags);
+        if (ok && count > 0) ok = mbar_wait(g_done, (uint32_t)((count - 1) & 1), f.flags);
         __syncwarp();
         tmem_fence_after();
         // The saved outputs carry the rounding of the forward's weights; grad_k, grad_v and
@@ -357,8 +375,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         bool ok = true;
         Ring v(NS);
         for (int i = 0; i < count; ++i, v.next()) {
-            const int b = i & 1;
-            ok = mbar_wait(&p_full[b], (uint32_t)((i >> 1) & 1), f.flags);
+            ok = mbar_wait(p_full, (uint32_t)(i & 1), f.flags);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (elect_one()) {
@@ -367,11 +384,13 @@ __global__ void __launch_bounds__(kAbThreads, 1)
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int k = 0; k < kAmKeys / 16; ++k)
-                        umma_f16_ta(tmem + 320 + 64 * m, tmem + 192 + 64 * b + 32 * m + 8 * k,
-                                    umma_desc_of(kb + m * (kAmKBytes >> 4) + k * (2048 >> 4), d_hi),
+                    for (int k = 0; k < 2 * (kAmKeys / 16); ++k)      // high parts, low parts
+                        umma_f16_ta(tmem + 320 + 64 * m,
+                                    tmem + 192 + 64 * (k >> 2) + 32 * m + 8 * (k & 3),
+                                    umma_desc_of(kb + m * (kAmKBytes >> 4) + (k & 3) * (2048 >> 4),
+                                                 d_hi),
                                     id_q, (i | k) != 0 ? 1u : 0u);
-                umma_commit(&g_done[b]);
+                umma_commit(g_done);
                 umma_commit(&kv_empty[v.st]);
             }
             __syncwarp();

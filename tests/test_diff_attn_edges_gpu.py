@@ -76,3 +76,19 @@ def test_gradients_without_the_output():
     for a, b in zip(dcnb.diff_attn_grad(q, k, v, lam, None, saved, go),
                     dcnb.diff_attn_grad(q, k, v, lam, out, saved, go)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("shape,causal", [((1, 400, 400, 2, 1, 64, 64), True),
+                                          ((2, 300, 500, 2, 2, 32, 64), False)])
+def test_grad_q_is_rounded_once(shape, causal, dt):
+    """Root mean square error of grad_q against that of rounding the float64 result once,
+    which is 1.  Score gradients rounded to the type before their product would add an
+    error of the same size for every term: sqrt(2) and more.  What is left beside the last
+    rounding is the row sums' share (weights rounded in the forward pass; their errors
+    average over the keys, a quarter of a rounding): sqrt(1 + 1/16) = 1.03."""
+    q, k, v, lam, go = inputs(*shape, DT[dt], 25)
+    want = ref.attn(q, k, v, lam, causal=causal, grad_out=go)["q"][0]
+    got = grads_of(q, k, v, lam, go, causal=causal)[0].double().cpu()
+    once = want.to(DT[dt]).double()
+    assert (got - want).norm() <= 1.25 * (once - want).norm()
