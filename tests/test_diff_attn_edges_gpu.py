@@ -92,3 +92,20 @@ def test_grad_q_is_rounded_once(shape, causal, dt):
     got = grads_of(q, k, v, lam, go, causal=causal)[0].double().cpu()
     once = want.to(DT[dt]).double()
     assert (got - want).norm() <= 1.25 * (once - want).norm()
+
+
+@pytest.mark.parametrize("Lq,Lk,M,Mk", [(2048, 128, 8, 1), (40, 8192, 2, 2)])
+def test_long_float32_sums_of_gradients(Lq, Lk, M, Mk):
+    """Root mean square errors of float32 gradients that sum many terms (grad_k and grad_v
+    2048 tokens of 8 heads, grad_q 8192 keys).  A float32 addition's rounding error is
+    2.6e-8 of the sum on average, so n additions one after another of terms with random
+    signs are off by 2.6e-8 sqrt(n / 2): 2.4e-6 for 16384 terms, 1.7e-6 for 8192.  Sums of
+    64 first, then of those, are off by 2.6e-8 (sqrt(32) + sqrt(n / 128)), at most 4.4e-7;
+    the terms themselves (a dot product of 32, an exponential) by 6e-7.  Together 7.5e-7."""
+    q, k, v, lam, go = inputs(1, Lq, Lk, M, Mk, 32, 32, torch.float32, 26)
+    r = ref.attn(q, k, v, lam, grad_out=go)
+    got = dict(zip("qkv", grads_of(q, k, v, lam, go)))
+    for name in ("kv" if Lq > Lk else "q"):
+        want = r[name][0]
+        off = (got[name].double().cpu() - want).norm() / want.norm()
+        assert off <= 1e-6, f"grad_{name}: {float(off):.2e}"
