@@ -228,12 +228,14 @@ __device__ __forceinline__ void attn_weighted(const float* A, int lda, const flo
     }
 }
 
-// The same with the tile's sum formed first: a sum of n terms then takes its rounding from
-// n / 64 additions to a large value instead of n (of random signs, sqrt(n) errors of the
-// sum's own step: 16384 rows gave grad_k an error of 2.3e-6, now less than 1e-6).
+// The tile's sum formed first: acc = acc * keep + sum.  A sum of n terms then takes its
+// rounding from n / 64 additions to a large value instead of n (of random signs, sqrt(n)
+// errors of the sum's own step: 16384 rows gave grad_k an error of 2.3e-6, now less than
+// 1e-6, and 8192 keys an output 1.7e-6).
 template <int RT, int CT>
 __device__ __forceinline__ void attn_weighted_tile(const float* A, int lda, const float* B,
-                                                   int ldb, int n, float (&acc)[RT][CT]) {
+                                                   int ldb, int n, float (&acc)[RT][CT],
+                                                   const float (&keep)[RT]) {
     float part[RT][CT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -243,7 +245,16 @@ __device__ __forceinline__ void attn_weighted_tile(const float* A, int lda, cons
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) acc[r][c] += part[r][c];
+        for (int c = 0; c < CT; ++c) acc[r][c] = fmaf(acc[r][c], keep[r], part[r][c]);
+}
+
+template <int RT, int CT>
+__device__ __forceinline__ void attn_weighted_tile(const float* A, int lda, const float* B,
+                                                   int ldb, int n, float (&acc)[RT][CT]) {
+    float one[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) one[r] = 1.f;
+    attn_weighted_tile<RT, CT>(A, lda, B, ldb, n, acc, one);
 }
 
 template <int CT>
@@ -262,8 +273,12 @@ __host__ __device__ constexpr int attn_fwd_smem(int BQ, int D, int CT) {
     return (BQ * attn_ld(2, D) + (kk > kp ? kk : kp) + kAttnKeys * attn_ldv(CT)) * 4 + kAttnKeys;
 }
 
+// Two blocks a multiprocessor for 16 rows and for values up to 32 channels: one block (139
+// and 148 registers) took 1258 us against 912 on one float32 token over 16 caches of 8192
+// keys, and 260 against 199 on the case above.
 template <typename T, int BQ, int CT>
-__global__ void __launch_bounds__(kAttnThreads) diff_attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, BQ == 16 || CT == 2 ? 2 : 1)
+    diff_attn_kernel(const AttnArgs a) {
     constexpr int RT = BQ / 16, BK = kAttnKeys;
     extern __shared__ __align__(16) float attn_smem[];
     const int D = a.D, D4 = (D + 3) & ~3, Dv = a.Dv;
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(kAttnThreads) diff_attn_kernel(const AttnArgs 
         attn_stage_keys<T>(a, kb, a.k_row, kv, j0, BK, 2, D, Ks, ldq, D4, ok);
         attn_stage_keys<T>(a, vb, a.v_row, kv, j0, BK, 1, Dv, Vs, ldv, 0, ok);
         __syncthreads();
-        float sc[2][RT][4];
+        float sc[2][RT][4], kept[2][RT];
         attn_dots<RT, 4>(Qs, ldq, Ks, ldq, D4, sc[0]);
         attn_dots<RT, 4>(Qs + D4, ldq, Ks + D4, ldq, D4, sc[1]);
         __syncthreads();                  // the keys are read: their place takes the scores
@@ -348,13 +363,12 @@ __global__ void __launch_bounds__(kAttnThreads) diff_attn_kernel(const AttnArgs 
 #pragma unroll
                 for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
                 l[s][r] = l[s][r] * keep + sum;
-#pragma unroll
-                for (int c = 0; c < CT; ++c) o[s][r][c] *= keep;
+                kept[s][r] = keep;
             }
         }
         __syncthreads();
-        attn_weighted<RT, CT>(Ps, ldp, Vs, ldv, BK, o[0]);
-        attn_weighted<RT, CT>(Ps + BQ * ldp, ldp, Vs, ldv, BK, o[1]);
+        attn_weighted_tile<RT, CT>(Ps, ldp, Vs, ldv, BK, o[0], kept[0]);
+        attn_weighted_tile<RT, CT>(Ps + BQ * ldp, ldp, Vs, ldv, BK, o[1], kept[1]);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {

@@ -109,3 +109,14 @@ def test_long_float32_sums_of_gradients(Lq, Lk, M, Mk):
         want = r[name][0]
         off = (got[name].double().cpu() - want).norm() / want.norm()
         assert off <= 1e-6, f"grad_{name}: {float(off):.2e}"
+
+
+def test_long_float32_sums_of_values():
+    """The maps' outputs over 8192 keys in one go (enough heads that the keys are not split):
+    1.7e-6 for additions one after another, 4.4e-7 in tiles, the weights' own 6e-7."""
+    q, k, v, lam, _ = inputs(1, 4, 8192, 160, 160, 8, 8, torch.float32, 27)
+    assert dcnb.diff_attn_forward_workspace_size(1, 4, 8192, 160, 160, 8, 8, 0) == 0
+    _, (maps, _) = dcnb.diff_attn(q, k, v, lam, save=True)
+    want = ref.attn(q, k, v, lam)["maps"][0]
+    off = (maps.double().cpu() - want).norm() / want.norm()
+    assert off <= 1e-6, f"{float(off):.2e}"
