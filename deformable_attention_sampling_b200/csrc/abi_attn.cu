@@ -247,7 +247,11 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Key splits of the tensor-core forward: one CTA a multiprocessor runs, so the
 // keys are split when the tiles leave half of them idle or more, at least two
-// key tiles each.
+// key tiles each.  Measured in bf16 (split / not, us): 300 tokens of 2 images, 4 heads
+// of 32 + 64, over 300 keys 16.0 / 10.3, 512 16.4 / 12.4, 1024 18.9 / 19.3, 4096
+// 25.5 / 65.8; 128 tokens of 8 heads of 64 + 128 over 300 keys 16.5 / 11.0, 1024
+// 17.5 / 19.8, 4096 22.2 / 62.5.  The join costs more than a split saves below about
+// 1000 keys.
 int mma_splits(int N, int Lq, int Lk, int M, int Dv) {
     const long long ctas = (long long)ceil_div(Lq, dcnb::kAmRows) * N * M *
                            ceil_div(Dv, dcnb::kAmMaxDv);
@@ -293,7 +297,14 @@ const void* step_kernel(int D, int Dv) {
     }
 }
 
-// Tokens from which the 128-row tiles of the tensor-core forward are taken.
+// Tokens from which the 128-row tiles of the tensor-core kernels are taken.
+// Measured in bf16, heads of 64 + 128 (tensor-core / few-token kernel, us): one image,
+// 16 heads of 4 key / value heads, 4096 keys: 8 tokens 18.7 / 16.0, 16 tokens 18.8 /
+// 24.6, 17 tokens 19.0 / 27.8, 64 tokens 20.8 / 59.0; over 300 keys the other way
+// round, 17 tokens 12.4 / 8.7, 64 tokens 14.2 / 12.0.  16 images of 8 + 8 heads, 4096
+// keys: 8 tokens 70 / 69, 16 tokens 70 / 103, 17 tokens 70 / 153.  The gradients take
+// the same number, but there the other form is the CUDA cores': at 16 tokens 28 / 142
+// over 300 keys, 92 / 1314 over 4096.
 constexpr int kMmaMinTokens = 17;
 
 // The gradient kernels' tensor-core form: heads and values that its TMEM holds.

@@ -21,6 +21,7 @@
 // 128 (201 MB: 4.1 TB/s; 31 us at the measured copy rate), 10 us for the join.
 // Held by a warp's chain of loads, 8 dependent score products and shuffles: the
 // time hardly depends on the split (4 to 27 parts: 57 to 64 us with the join).
+// Weights enter the value product rounded to the type, as in diff_attn_mma.cuh.
 // The keys are split over CTAs (and the 4 warps of a CTA, which join in shared
 // memory); diff_attn_join_kernel adds the CTAs' parts in a fixed order.
 #pragma once

@@ -8,7 +8,9 @@
 //
 // Measured: 34 us for 64 x 3136 x 64 in fp16 (103 MB, 16 us at the measured copy
 // rate), 85 us forward and 141 + 10 us backward for 8 x 4096 x 1024 in bf16 (268
-// and 403 MB): a team's sums, not the bytes, set the step.
+// and 403 MB): a team's sums, not the bytes, set the step.  Longer rows, 67 MB a
+// tensor in bf16 (floors 41 and 61 us): 8192 x 4096 forward 88, backward 178 us; 4096
+// x 8192 forward 130, backward 391 us, whose blocks of 1024 threads spill (below).
 // Bound: HBM.  One pass over the rows: x and y are read once, z and h written
 // once, the rows' statistics stay in registers (two-pass: the mean first, then
 // the squared deviations, so that a large mean costs no digits), and h is the
@@ -25,6 +27,9 @@
 // and the factors' gradients from four column sums per image,
 //   A = sum_l g * n1, B = sum_l g, E = sum_l grad_h * n2, F = sum_l grad_h:
 //   grad_gate = scale * (post_weight * A + post_bias * B), and so on.
+// h was the norm of z before its rounding; n2 here is that of z as stored.  That
+// costs 16-bit gradients 1.4 times the error of rounding them once; the unrounded z
+// would have to be saved in float32, or formed again from x and the first norm.
 // Every block sums its rows of one image in registers and writes one partial
 // row; a second kernel adds the partials in a fixed order, so the gradients do
 // not depend on the order in which blocks run.
@@ -177,8 +182,10 @@ struct TeamSum {
 };
 
 // Blocks of 256 threads (rows of up to 2048 channels) and of 512 (up to 4096)
-// have 128 registers a thread, which hold every factor and the next row; longer
-// rows take 1024 threads at 64.
+// have 128 registers a thread, which hold every factor and the next row of 16-bit
+// data; float32 rows (32 to 136 bytes) and the element-wise 16-bit gradient (96 or
+// 128 bytes) spill a little.  Longer rows take 1024 threads at 64 registers and spill
+// 324 to 640 bytes.
 constexpr int kNormSmall = 256;
 constexpr int kNormMiddle = 512;
 

@@ -650,7 +650,11 @@ DCN_API long long diff_attn_backward_workspace_size(int N, int Lq, int Lk, int M
  * as out).  The gradients are dense: grad_q [N][Lq][M][2][D], grad_k
  * [N][Lk][Mk][2][D], grad_v [N][Lk][Mk][Dv], grad_lambda [M]; those of a key /
  * value head are summed over its M / Mk heads.  Keys that no token sees get
- * zeros.  No sum goes through atomics: equal calls give equal bits.
+ * zeros.  No sum goes through atomics: equal calls give equal bits.  With 16-bit
+ * data on the tensor cores the score gradients enter grad_k's product, and P_0 -
+ * lambda P_1 grad_v's, rounded to that type (fp16 ones scaled by powers of two per
+ * image and key / value head).  k and v are required whenever N * Lk > 0, the
+ * other inputs whenever N * Lq > 0.
  * Arguments, limits and errors otherwise as diff_attn_forward.
  */
 DCN_API int diff_attn_backward(const void* q, const void* k, const void* v, const void* lambda,
